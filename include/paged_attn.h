@@ -13,7 +13,7 @@
  *
  * Entry points
  * ------------
- *  the path:   paged_expand_ubatch, paged_kv_append, paged_attn_plan,
+ *  the path:   paged_batch_build, paged_expand_ubatch, paged_kv_append, paged_attn_plan,
  *              paged_attn_prefill, paged_attn_decode, paged_attn_decode_append,
  *              paged_attn_run, paged_attn_forward, paged_attn_forward_noalloc
  *  around it:  paged_attn_workspace_size, paged_attn_validate,
@@ -81,7 +81,10 @@ extern "C" {
 #define PA_ERR_KV_RANGE 0x2     /* tok_kv_len[t] < 0 or > max_pages * P */
 #define PA_ERR_SLOT_RANGE 0x4   /* slot_mapping[t] >= num_pages * P */
 #define PA_ERR_TIMEOUT 0x8      /* a bounded device-side wait gave up */
-#define PA_ERR_SEQ_RANGE 0x10   /* expansion: tok_seq[t] >= n_seq or position beyond the row */
+#define PA_ERR_SEQ_RANGE 0x10   /* expansion: tok_seq[t] >= n_seq or position beyond the row;
+                                   batch build: a request's lengths do not fit its row */
+#define PA_ERR_NO_SPACE 0x20    /* batch build: requests left out (free pages or tokens ran out) */
+#define PA_ERR_REFCOUNT 0x40    /* batch build: a finished row names a page that is free */
 
 /* Human-readable text of a status code (static storage). */
 const char *paged_attn_strerror(int status);
@@ -109,6 +112,48 @@ int paged_expand_ubatch(const int32_t *seq_page_table, int n_seq, int max_pages,
                         const int32_t *tok_seq, const int32_t *tok_pos, int T, int P,
                         int32_t *tok_page_table, int32_t *tok_kv_len, int64_t *slot_mapping,
                         int *err, void *stream);
+
+/*
+ * The tables of a serving step, built on the device from request lengths: continuous
+ * batching without a host round trip (graph-capturable; the page section 作品简介 builds
+ * these tables on the host).  The device counterpart of pa_pool_alloc / pa_pool_release
+ * followed by paged_expand_ubatch, with the same results: pages are handed out lowest id
+ * first, and a page is free while its reference count is 0.
+ *
+ *   seq_page_table [n_seq][max_pages] int32 (in/out)  request i's row holds the pages of
+ *       its cached positions in entries 0 .. ceil(seq_len[i] / P) - 1
+ *   seq_len [n_seq] int32   cached positions of each request
+ *   new_len [n_seq] int32   positions that the step adds: 0 none, 1 a decoding request, more
+ *       a chunk of a prompt; < 0: the request has finished
+ *   page_ref [num_pages] int32 (in/out, 16-byte aligned)  reference count of every page
+ *   q_start [n_seq + 1] int32 (out)   first token of each request; q_start[n_seq] is the
+ *       number of tokens of the step
+ *   seq_len_out [n_seq] int32 (out)   seq_len plus the admitted new positions (0 for a
+ *       finished request); may be seq_len itself
+ *   tok_seq, tok_pos, tok_kv_len [T] int32, tok_page_table [T][max_pages] int32,
+ *   slot_mapping [T] int64 (out)      as paged_expand_ubatch takes and gives them, tokens in
+ *       request order; entries past the last token are padding (-1, 0, 0, -1, -1)
+ *   err (device, optional, may be NULL): PA_ERR_* bits are OR-ed in
+ *
+ * In this order:
+ *   1. every page in a finished request's row loses one reference and the row becomes -1
+ *      (a page that is free already: PA_ERR_REFCOUNT; an id outside the pool:
+ *      PA_ERR_PAGE_RANGE; neither is counted);
+ *   2. a request with seq_len < 0, or with seq_len + new_len past its row, adds nothing
+ *      (PA_ERR_SEQ_RANGE);
+ *   3. the requests are admitted in order up to the first whose new pages exceed the free
+ *      pages left or whose tokens exceed T; it and every later one add nothing
+ *      (PA_ERR_NO_SPACE).  q_start tells which: put the requests that must go on first;
+ *   4. an admitted request's new pages (those of its positions past ceil(seq_len / P) * P)
+ *      are taken with reference count 1 and written behind its last entry.
+ * A request must own its last, partly filled page (pa_pool_fork).  The arrays must not
+ * overlap, but for seq_len_out.  n_seq <= 16384 (else PA_EUNSUPPORTED).  Two launches.
+ */
+int paged_batch_build(int32_t *seq_page_table, int n_seq, int max_pages, const int32_t *seq_len,
+                      const int32_t *new_len, int32_t *page_ref, int num_pages, int P, int T,
+                      int32_t *q_start, int32_t *seq_len_out, int32_t *tok_seq, int32_t *tok_pos,
+                      int32_t *tok_page_table, int32_t *tok_kv_len, int64_t *slot_mapping,
+                      int *err, void *stream);
 
 /*
  * reshape-and-cache (CacheFlow page, section 核心架构 3): write the new K and V

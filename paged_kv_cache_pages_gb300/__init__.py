@@ -8,6 +8,8 @@ must have been built (``paged_kv_cache_pages_gb300.build.build()`` or
 is no fallback.
 
 Entry points mirror include/paged_attn.h:
+  batch_build     a step's tables, token lists and slots from request lengths, pages taken
+                  from a reference-counted pool on the device
   expand_ubatch   per-token page-table / kv_len expansion + slot mapping
   kv_append       reshape-and-cache into the paged pool
   copy_pages      page copy of a copy-on-write fork
@@ -21,8 +23,10 @@ Entry points mirror include/paged_attn.h:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -39,6 +43,7 @@ PA_OK, PA_EINVAL, PA_EUNSUPPORTED, PA_EWORKSPACE = 0, -1, -2, -3
 PA_ELAUNCH, PA_EDEVICE, PA_EALIGN, PA_ENOSPACE = -4, -5, -6, -7
 PA_ERR_PAGE_RANGE, PA_ERR_KV_RANGE, PA_ERR_SLOT_RANGE = 0x1, 0x2, 0x4
 PA_ERR_TIMEOUT, PA_ERR_SEQ_RANGE = 0x8, 0x10
+PA_ERR_NO_SPACE, PA_ERR_REFCOUNT = 0x20, 0x40
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 
@@ -47,6 +52,7 @@ _SIGS = {
     "paged_attn_strerror": ([_i], ctypes.c_char_p),
     "paged_attn_version": ([], _i),
     "paged_expand_ubatch": ([_vp, _i, _i, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp], _i),
+    "paged_batch_build": ([_vp, _i, _i, _vp, _vp, _vp, _i, _i, _i] + [_vp] * 9, _i),
     "paged_kv_append": ([_vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _vp, _vp], _i),
     "paged_attn_workspace_size": ([_i, _i, _i, _i], _sz),
     "paged_attn_plan": ([_vp, _i, _vp, _i, _i, _i, _i, _i, _vp, _sz, _vp], _i),
@@ -128,6 +134,23 @@ def _req(t, dtype, name):
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
 
 
+def _req_on(t, dtype, shape, device, name):
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device \
+            or device.type != "cuda":
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         "one CUDA device")
+
+
+def _on(t):
+    """The tensor's device as the current one while a call is made (launches, the SM count
+    and the default stream go by the current device)."""
+    return _HERE_ALREADY if t.device.index == torch.cuda.current_device() \
+        else torch.cuda.device(t.device)
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
 def workspace_size(T: int, Hq: int, Hkv: int, d: int) -> int:
     return int(_lib.paged_attn_workspace_size(T, Hq, Hkv, d))
 
@@ -156,6 +179,56 @@ def expand_ubatch(seq_page_table, tok_seq, tok_pos, P, out=None, err=None, strea
                                     _ptr(tok_pos), T, P, _ptr(tpt), _ptr(kv), _ptr(slot),
                                     _ptr(err), _stream(stream)), "paged_expand_ubatch")
     return tpt, kv, slot
+
+
+class Batch(NamedTuple):
+    """What batch_build leaves: first token of each request [n_seq + 1], each request's
+    length after the step [n_seq], and the tokens' lists and tables [T]."""
+    q_start: torch.Tensor
+    seq_len: torch.Tensor
+    tok_seq: torch.Tensor
+    tok_pos: torch.Tensor
+    tok_page_table: torch.Tensor
+    tok_kv_len: torch.Tensor
+    slot_mapping: torch.Tensor
+
+
+def new_batch(n_seq: int, max_pages: int, T: int, device=None) -> Batch:
+    """Output buffers of batch_build for up to T tokens of n_seq requests."""
+    dev = device or "cuda"
+
+    def i32(*shape):
+        return torch.empty(shape, dtype=torch.int32, device=dev)
+    return Batch(i32(n_seq + 1), i32(n_seq), i32(T), i32(T), i32(T, max_pages), i32(T),
+                 torch.empty(T, dtype=torch.int64, device=dev))
+
+
+def batch_build(seq_page_table, seq_len, new_len, page_ref, P, T, out=None, err=None,
+                stream=None) -> Batch:
+    """One serving step's tables from request lengths (see paged_batch_build): requests with
+    new_len < 0 give their pages back, the longest prefix of the others that fits T tokens and
+    the free pages is admitted, and its tokens' lists are written.  seq_page_table and
+    page_ref are updated in place."""
+    n_seq, max_pages = seq_page_table.shape
+    for t, shape, n in ((seq_page_table, (n_seq, max_pages), "seq_page_table"),
+                        (seq_len, (n_seq,), "seq_len"), (new_len, (n_seq,), "new_len"),
+                        (page_ref, (page_ref.numel(),), "page_ref")):
+        _req_on(t, torch.int32, shape, seq_page_table.device, n)
+    if out is None:
+        out = new_batch(n_seq, max_pages, T, seq_page_table.device)
+    else:
+        for t, shape, n in zip(out, ((n_seq + 1,), (n_seq,), (T,), (T,), (T, max_pages), (T,),
+                                     (T,)), Batch._fields):
+            _req_on(t, torch.int64 if n == "slot_mapping" else torch.int32, shape,
+                    seq_page_table.device, n)
+    if err is not None:
+        _req_on(err, torch.int32, (err.numel(),), seq_page_table.device, "err")
+    with _on(seq_page_table):
+        _check(_lib.paged_batch_build(
+            seq_page_table.data_ptr(), n_seq, max_pages, seq_len.data_ptr(), new_len.data_ptr(),
+            page_ref.data_ptr(), page_ref.numel(), P, T, *[t.data_ptr() for t in out],
+            None if err is None else err.data_ptr(), _stream(stream)), "paged_batch_build")
+    return out
 
 
 def kv_append(k, v, slot_mapping, k_pages, v_pages, err=None, stream=None):

@@ -143,6 +143,45 @@ int paged_expand_ubatch(const int32_t *seq_page_table, int n_seq, int max_pages,
   return launch_status(cudaGetLastError());
 }
 
+int paged_batch_build(int32_t *seq_page_table, int n_seq, int max_pages, const int32_t *seq_len,
+                      const int32_t *new_len, int32_t *page_ref, int num_pages, int P, int T,
+                      int32_t *q_start, int32_t *seq_len_out, int32_t *tok_seq, int32_t *tok_pos,
+                      int32_t *tok_page_table, int32_t *tok_kv_len, int64_t *slot_mapping,
+                      int *err, void *stream) {
+  NvtxRange nvtx_range("paged_batch_build");
+  if (n_seq < 0 || max_pages <= 0 || num_pages < 0 || P <= 0 || T < 0) return PA_EINVAL;
+  if (n_seq > kBatchMaxSeq || (int64_t)max_pages * P > INT_MAX / 2 || T > INT_MAX / 2)
+    return PA_EUNSUPPORTED;
+  if (!q_start) return PA_EINVAL;
+  if (n_seq > 0 && (!seq_page_table || !seq_len || !new_len || !seq_len_out)) return PA_EINVAL;
+  if (num_pages > 0 && !page_ref) return PA_EINVAL;
+  if (T > 0 && (!tok_seq || !tok_pos || !tok_page_table || !tok_kv_len || !slot_mapping))
+    return PA_EINVAL;
+  if (!aligned16(seq_page_table) || !aligned16(page_ref) || !aligned16(tok_page_table))
+    return PA_EALIGN;
+  BatchArgs a;
+  a.seq_pt = seq_page_table;
+  a.seq_len = seq_len;
+  a.new_len = new_len;
+  a.page_ref = page_ref;
+  a.q_start = q_start;
+  a.seq_len_out = seq_len_out;
+  a.tok_seq = tok_seq;
+  a.tok_pos = tok_pos;
+  a.tok_pt = tok_page_table;
+  a.tok_kv = tok_kv_len;
+  a.slot = slot_mapping;
+  a.err = err;
+  a.n_seq = n_seq;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.P = P;
+  a.T = T;
+  const int sms = sm_count();
+  if (sms <= 0) return PA_ELAUNCH;
+  return launch_status(launch_batch(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
 int paged_kv_append(const uint16_t *k, const uint16_t *v, const int64_t *slot_mapping, int T,
                     uint16_t *k_pages, uint16_t *v_pages, int num_pages, int Hkv, int P, int d,
                     int *err, void *stream) {

@@ -67,6 +67,21 @@ struct AttnArgs {
   const int64_t *slot;
 };
 
+// Arguments of the batch build (passed by value); see paged_batch_build.
+constexpr int kBatchMaxSeq = 16384;  // two sums per request in one CTA's shared memory
+struct BatchArgs {
+  int32_t *seq_pt;
+  const int32_t *seq_len, *new_len;
+  int32_t *page_ref;
+  int32_t *q_start, *seq_len_out, *tok_seq, *tok_pos, *tok_pt, *tok_kv;
+  int64_t *slot;
+  int *err;
+  int n_seq, max_pages, num_pages, P, T;
+};
+
+// The two launches of the batch build.
+cudaError_t launch_batch(const BatchArgs &a, int num_sms, cudaStream_t s);
+
 // Decode: split-KV over all SMs plus the log-sum-exp reduce.  Returns a
 // cudaError_t from the launches.
 cudaError_t launch_decode(const AttnArgs &a, int num_sms, const void *tmaps, cudaStream_t s);
