@@ -26,6 +26,11 @@
  *              paged_attn_decode_fp8, paged_attn_prefill_fp8 and
  *              paged_attn_forward_fp8 (FP8 pages); paged_copy_pages and
  *              pa_pool_fork (copy-on-write forks of shared pages)
+ *  other attentions over the same pages:  paged_attn_diff_workspace_size,
+ *              paged_attn_plan_diff, paged_attn_diff_run, paged_attn_diff_forward
+ *              (differential attention); paged_attn_plan_window,
+ *              paged_attn_window_run, paged_attn_window_forward (a window over
+ *              the last positions, with sinks)
  *
  * Conventions shared by every call
  * --------------------------------
@@ -85,6 +90,7 @@ extern "C" {
                                    batch build: a request's lengths do not fit its row */
 #define PA_ERR_NO_SPACE 0x20    /* batch build: requests left out (free pages or tokens ran out) */
 #define PA_ERR_REFCOUNT 0x40    /* batch build: a finished row names a page that is free */
+#define PA_ERR_PLAN 0x80        /* the workspace holds the plan of another operator */
 
 /* Human-readable text of a status code (static storage). */
 const char *paged_attn_strerror(int status);
@@ -423,6 +429,90 @@ int paged_attn_forward_fp8(const uint16_t *q, const uint8_t *k8_pages, const uin
                            const int32_t *tok_kv_len, int T, int Hq, int Hkv, int P, int d,
                            int num_pages, float scale, uint16_t *out, void *workspace,
                            size_t workspace_bytes, void *stream);
+
+/*
+ * Differential attention over the pages: the difference of two softmax maps, with a learned
+ * weight per query head and an optional norm per head.  Tokens and chunks as in
+ * paged_attn_forward (single tokens on the split-KV kernel, runs of tokens on the tensor-core
+ * tiles).  A query row is (q1 | q2) and a cached K row (k1 | k2), halves of d / 2; a V row
+ * holds d values.  For query head h of token t, KV head g = h / (Hq / Hkv), j < tok_kv_len[t]:
+ *
+ *   A_i = softmax_j(scale * q_i . k_i[j]),  i = 1, 2
+ *   y   = sum_j (A_1[j] - lam[h] A_2[j]) V[j]
+ *   out[t][h] = out_scale * y                                           (norm_weight NULL)
+ *   out[t][h] = out_scale * y / sqrt(mean(y^2) + eps) * norm_weight     (elementwise over d)
+ *
+ * with binary32 sums, softmax statistics and norms; each map's probabilities are rounded to
+ * binary16 for the product with V, as in paged_attn_forward.  tok_kv_len 0 gives a zero row.
+ *   lam [Hq] float (device)           the weight of each head's second map, as computed from
+ *       the learned vectors (exp(a1 . b1) - exp(a2 . b2) + its initial value)
+ *   norm_weight [d] float (device), or NULL
+ *   eps   >= 0; out_scale: any (1 minus the initial weight, usually)
+ *   scale > 0 and finite (usually 1 / sqrt(d / 2))
+ *   other arguments as paged_attn_forward: d in {64, 128} is the whole row, K and V pages
+ *   have the same layout, and paged_kv_append writes them.
+ *
+ * A plan of this operator has its own layout: make the workspace
+ * paged_attn_diff_workspace_size bytes long and plan with paged_attn_plan_diff (arguments as
+ * paged_attn_plan; one plan serves every layer).  paged_attn_diff_run runs on that plan; on
+ * another operator's it sets PA_ERR_PLAN and writes nothing.  paged_attn_diff_forward is
+ * the plan followed by the run.
+ */
+size_t paged_attn_diff_workspace_size(int T, int Hq, int Hkv, int d);
+int paged_attn_plan_diff(const int32_t *tok_page_table, int max_pages, const int32_t *tok_kv_len,
+                         int T, int Hq, int Hkv, int P, int d, void *workspace,
+                         size_t workspace_bytes, void *stream);
+int paged_attn_diff_run(const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
+                        const int32_t *tok_page_table, int max_pages, const int32_t *tok_kv_len,
+                        int T, int Hq, int Hkv, int P, int d, int num_pages, float scale,
+                        const float *lam, const float *norm_weight, float eps, float out_scale,
+                        uint16_t *out, void *workspace, size_t workspace_bytes, void *stream);
+int paged_attn_diff_forward(const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
+                            const int32_t *tok_page_table, int max_pages,
+                            const int32_t *tok_kv_len, int T, int Hq, int Hkv, int P, int d,
+                            int num_pages, float scale, const float *lam,
+                            const float *norm_weight, float eps, float out_scale, uint16_t *out,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Attention of single tokens and chunks to the last `window` positions, with an optional
+ * learned sink per query head.  With lo = max(0, tok_kv_len[t] - window):
+ *
+ *   out[t][h] = sum_{lo <= j < tok_kv_len[t]} e^{x_j} V[j] / (sum_j e^{x_j} + e^{sink[h]}),
+ *   x_j = scale * q[t][h] . K[j]
+ *
+ * (window 1: the token's own position alone; a window of the row's capacity or more: plain
+ * causal attention).  tok_kv_len 0 gives a zero row.
+ *   window >= 1
+ *   sink [Hq] float (device), or NULL for none
+ *   scale > 0 and finite
+ *   other arguments as paged_attn_forward.
+ *
+ * Key blocks before a token's window are not read, and neither are the table's entries for
+ * pages that lie wholly before the windows of the tokens that share a tile (a tile's tokens
+ * are consecutive and have identical rows): such pages may have been given back.  Cells
+ * before a window never reach the output, whatever they hold.
+ *
+ * paged_attn_plan_window plans with a window (workspace as paged_attn_workspace_size; one
+ * plan serves every layer with that window); paged_attn_window_run runs on it, with the
+ * plan's window, and on another plan sets PA_ERR_PLAN and writes nothing.  The plain run and
+ * its prefill refuse a windowed plan in the same way.  paged_attn_window_forward is the plan
+ * followed by the run.
+ */
+int paged_attn_plan_window(const int32_t *tok_page_table, int max_pages,
+                           const int32_t *tok_kv_len, int T, int Hq, int Hkv, int P, int d,
+                           int window, void *workspace, size_t workspace_bytes, void *stream);
+int paged_attn_window_run(const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
+                          const int32_t *tok_page_table, int max_pages,
+                          const int32_t *tok_kv_len, int T, int Hq, int Hkv, int P, int d,
+                          int num_pages, float scale, const float *sink, uint16_t *out,
+                          void *workspace, size_t workspace_bytes, void *stream);
+int paged_attn_window_forward(const uint16_t *q, const uint16_t *k_pages,
+                              const uint16_t *v_pages, const int32_t *tok_page_table,
+                              int max_pages, const int32_t *tok_kv_len, int T, int Hq, int Hkv,
+                              int P, int d, int num_pages, float scale, int window,
+                              const float *sink, uint16_t *out, void *workspace,
+                              size_t workspace_bytes, void *stream);
 
 /*
  * Page copy for copy-on-write forks (CacheFlow page, section 核心架构 2: blocks

@@ -18,6 +18,8 @@ Entry points mirror include/paged_attn.h:
   kv_append_fp8 / decode_fp8 / prefill_fp8 / forward_fp8   FP8 (E4M3) KV pages with
                   per-row scales
   plan / prefill / decode / run / forward   the attention itself
+  plan_diff / diff_run / diff_forward       differential attention over the same pages
+  plan_window / window_run / window_forward attention to the last positions, with sinks
   validate, read_error, set_prefill_min_run, workspace_size
   PagePool        host page allocator with reference-counted sharing
 """
@@ -43,7 +45,7 @@ PA_OK, PA_EINVAL, PA_EUNSUPPORTED, PA_EWORKSPACE = 0, -1, -2, -3
 PA_ELAUNCH, PA_EDEVICE, PA_EALIGN, PA_ENOSPACE = -4, -5, -6, -7
 PA_ERR_PAGE_RANGE, PA_ERR_KV_RANGE, PA_ERR_SLOT_RANGE = 0x1, 0x2, 0x4
 PA_ERR_TIMEOUT, PA_ERR_SEQ_RANGE = 0x8, 0x10
-PA_ERR_NO_SPACE, PA_ERR_REFCOUNT = 0x20, 0x40
+PA_ERR_NO_SPACE, PA_ERR_REFCOUNT, PA_ERR_PLAN = 0x20, 0x40, 0x80
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 
@@ -89,6 +91,13 @@ _SIGS = {
     "paged_attn_plan_prefill": ([_vp, _i, _vp, _i, _i, _i, _i, _i, _vp, _sz, _vp], _i),
     "paged_attn_masked_prefill": ([_vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i,
                                    ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i),
+    "paged_attn_diff_workspace_size": ([_i, _i, _i, _i], _sz),
+    "paged_attn_plan_diff": ([_vp, _i, _vp, _i, _i, _i, _i, _i, _vp, _sz, _vp], _i),
+    "paged_attn_diff_run": (_ATTN_ARGS[:13] + [_vp, _vp, _f, _f] + _ATTN_ARGS[13:], _i),
+    "paged_attn_diff_forward": (_ATTN_ARGS[:13] + [_vp, _vp, _f, _f] + _ATTN_ARGS[13:], _i),
+    "paged_attn_plan_window": ([_vp, _i, _vp, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp], _i),
+    "paged_attn_window_run": (_ATTN_ARGS[:13] + [_vp] + _ATTN_ARGS[13:], _i),
+    "paged_attn_window_forward": (_ATTN_ARGS[:13] + [_i, _vp] + _ATTN_ARGS[13:], _i),
 }
 for _name, (_args, _res) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -450,6 +459,120 @@ def decode_append(q, k_new, v_new, slot_mapping, k_pages, v_pages, tok_page_tabl
         float(scale), _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
         "paged_attn_decode_append")
     return out
+
+
+def diff_workspace_size(T: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(_lib.paged_attn_diff_workspace_size(T, Hq, Hkv, d))
+
+
+def new_diff_workspace(T: int, Hq: int, Hkv: int, d: int, device=None) -> torch.Tensor:
+    """Workspace of the differential attention (plan_diff, diff_run, diff_forward)."""
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        n = diff_workspace_size(T, Hq, Hkv, d)
+        if n == 0:
+            raise PagedAttnError(PA_EUNSUPPORTED, "diff_workspace_size")
+        return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def _plan(fn_name, tok_page_table, tok_kv_len, Hq, Hkv, P, d, window, workspace, stream):
+    dev = tok_page_table.device
+    T, max_pages = tok_page_table.shape
+    _req_on(tok_page_table, torch.int32, (T, max_pages), dev, "tok_page_table")
+    _req_on(tok_kv_len, torch.int32, (T,), dev, "tok_kv_len")
+    _req_on(workspace, torch.uint8, (workspace.numel(),), dev, "workspace")
+    with _on(tok_page_table):
+        _check(getattr(_lib, fn_name)(tok_page_table.data_ptr(), max_pages, tok_kv_len.data_ptr(),
+                                      T, Hq, Hkv, P, d, *window, workspace.data_ptr(),
+                                      workspace.numel(), _stream(stream)), fn_name)
+
+
+def plan_diff(tok_page_table, tok_kv_len, Hq, Hkv, P, d, workspace, stream=None):
+    """plan for diff_run (workspace from new_diff_workspace)."""
+    _plan("paged_attn_plan_diff", tok_page_table, tok_kv_len, Hq, Hkv, P, d, (), workspace, stream)
+
+
+def plan_window(tok_page_table, tok_kv_len, Hq, Hkv, P, d, window, workspace, stream=None):
+    """plan for window_run: every token attends to its last `window` positions."""
+    _plan("paged_attn_plan_window", tok_page_table, tok_kv_len, Hq, Hkv, P, d, (int(window),),
+          workspace, stream)
+
+
+def _attn_on(fn_name, q, k_pages, v_pages, tok_page_table, tok_kv_len, scale, extra, vectors, out,
+             workspace, new_ws, stream):
+    """Checks and marshals an attention call whose own arguments (`extra`) stand between the
+    scale and the output; `vectors`: its float32 tensors, as (tensor or None, length, name)."""
+    dev = q.device
+    T, Hq, d = q.shape
+    N, Hkv, P, _ = k_pages.shape
+    max_pages = tok_page_table.shape[1]
+    _req_on(q, torch.float16, (T, Hq, d), dev, "q")
+    _req_on(k_pages, torch.float16, (N, Hkv, P, d), dev, "k_pages")
+    _req_on(v_pages, torch.float16, (N, Hkv, P, d), dev, "v_pages")
+    _req_on(tok_page_table, torch.int32, (T, max_pages), dev, "tok_page_table")
+    _req_on(tok_kv_len, torch.int32, (T,), dev, "tok_kv_len")
+    for t, n, name in vectors:
+        if t is not None:
+            _req_on(t, torch.float32, (n,), dev, name)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _req_on(out, torch.float16, (T, Hq, d), dev, "out")
+    if workspace is None:
+        workspace = new_ws(T, Hq, Hkv, d, dev)
+    else:
+        _req_on(workspace, torch.uint8, (workspace.numel(),), dev, "workspace")
+    with _on(q):
+        _check(getattr(_lib, fn_name)(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), tok_page_table.data_ptr(),
+            max_pages, tok_kv_len.data_ptr(), T, Hq, Hkv, P, d, N, scale, *extra, out.data_ptr(),
+            workspace.data_ptr(), workspace.numel(), _stream(stream)), fn_name)
+    return out
+
+
+def _diff(fn_name, q, k_pages, v_pages, tok_page_table, tok_kv_len, scale, lam, norm_weight, eps,
+          out_scale, out, workspace, stream):
+    return _attn_on(
+        fn_name, q, k_pages, v_pages, tok_page_table, tok_kv_len, scale,
+        (lam.data_ptr(), None if norm_weight is None else norm_weight.data_ptr(), eps, out_scale),
+        ((lam, q.shape[1], "lam"), (norm_weight, q.shape[2], "norm_weight")), out, workspace,
+        new_diff_workspace, stream)
+
+
+def diff_run(q, k_pages, v_pages, tok_page_table, tok_kv_len, scale, lam, norm_weight=None,
+             eps=1e-5, out_scale=1.0, out=None, workspace=None, stream=None):
+    """Differential attention on a plan from plan_diff.  q rows are (q1 | q2) and cached K rows
+    (k1 | k2), halves of d / 2: out = norm(softmax(q1 k1) V - lam softmax(q2 k2) V) * out_scale,
+    the norm (norm_weight [d]) over each head's d values; None: no norm."""
+    if workspace is None:
+        raise ValueError("diff_run needs the workspace that plan_diff planned in")
+    return _diff("paged_attn_diff_run", q, k_pages, v_pages, tok_page_table, tok_kv_len, scale,
+                 lam, norm_weight, eps, out_scale, out, workspace, stream)
+
+
+def diff_forward(q, k_pages, v_pages, tok_page_table, tok_kv_len, scale, lam, norm_weight=None,
+                 eps=1e-5, out_scale=1.0, out=None, workspace=None, stream=None):
+    """plan_diff then diff_run for one ubatch; returns out [T][Hq][d] float16."""
+    return _diff("paged_attn_diff_forward", q, k_pages, v_pages, tok_page_table, tok_kv_len, scale,
+                 lam, norm_weight, eps, out_scale, out, workspace, stream)
+
+
+def window_run(q, k_pages, v_pages, tok_page_table, tok_kv_len, scale, sink=None, out=None,
+               workspace=None, stream=None):
+    """Attention to the last positions of each token (the window of the plan, made by
+    plan_window); sink [Hq]: a logit per query head that joins the softmax with no value."""
+    if workspace is None:
+        raise ValueError("window_run needs the workspace that plan_window planned in")
+    return _attn_on("paged_attn_window_run", q, k_pages, v_pages, tok_page_table, tok_kv_len,
+                    scale, (None if sink is None else sink.data_ptr(),),
+                    ((sink, q.shape[1], "sink"),), out, workspace, None, stream)
+
+
+def window_forward(q, k_pages, v_pages, tok_page_table, tok_kv_len, scale, window, sink=None,
+                   out=None, workspace=None, stream=None):
+    """plan_window then window_run for one ubatch; returns out [T][Hq][d] float16."""
+    return _attn_on("paged_attn_window_forward", q, k_pages, v_pages, tok_page_table, tok_kv_len,
+                    scale, (int(window), None if sink is None else sink.data_ptr()),
+                    ((sink, q.shape[1], "sink"),), out, workspace, new_workspace, stream)
 
 
 def validate(tok_page_table, tok_kv_len, P, num_pages, err, stream=None):

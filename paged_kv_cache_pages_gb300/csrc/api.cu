@@ -1,6 +1,7 @@
 // C-ABI entry points of libpagedattn.so (declared in include/paged_attn.h).
 // Host-side argument checks, workspace layout, tensor-map encoding and launches.
 #include <atomic>
+#include <cfloat>
 #include <climits>
 #include <cstdio>
 #include <cuda.h>
@@ -55,23 +56,24 @@ int check_shape(int Hq, int Hkv, int P, int d) {
 
 int launch_status(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ELAUNCH; }
 
-// Common checks of the attention calls.
+// Common checks of the attention calls.  maps: softmax maps per query head (the workspace
+// counts a head once per map).
 int check_attn(const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
                const int32_t *tpt, int max_pages, const int32_t *kv, int T, int Hq, int Hkv, int P,
                int d, int num_pages, const uint16_t *out, const void *ws, size_t ws_bytes,
-               bool need_data) {
+               bool need_data, int maps = 1) {
   if (T < 0 || max_pages < 0 || num_pages < 0) return PA_EINVAL;
   int st = check_shape(Hq, Hkv, P, d);
   if (st != PA_OK) return st;
   if ((int64_t)max_pages * P > INT_MAX / 2) return PA_EUNSUPPORTED;
-  if ((int64_t)T * Hq > INT_MAX / 256) return PA_EUNSUPPORTED;
+  if ((int64_t)T * Hq * maps > INT_MAX / 256) return PA_EUNSUPPORTED;
   if (T == 0) return PA_OK;
   if (!tpt || !kv || (max_pages == 0)) return PA_EINVAL;
   if (need_data && (!q || !k_pages || !v_pages || !out || num_pages == 0)) return PA_EINVAL;
   if (!ws) return PA_EWORKSPACE;
   int C = sm_count();
   if (C <= 0) return PA_ELAUNCH;
-  if (ws_bytes < ws_layout(T, Hq, Hkv, d, C).total) return PA_EWORKSPACE;
+  if (ws_bytes < ws_layout(T, Hq * maps, Hkv, d, C).total) return PA_EWORKSPACE;
   if (!aligned16(ws) || !aligned16(tpt) || !aligned16(kv)) return PA_EALIGN;
   if (need_data && (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out)))
     return PA_EALIGN;
@@ -103,6 +105,10 @@ AttnArgs make_args(const uint16_t *q, const uint16_t *k_pages, const uint16_t *v
   a.wait_ns = g_decode_wait_ns.load();
   a.k_new = a.v_new = nullptr;
   a.slot = nullptr;
+  a.lam = a.norm_w = a.sink = nullptr;
+  a.eps = 0.f;
+  a.out_scale = 1.f;
+  a.windowed = false;
   return a;
 }
 
@@ -207,7 +213,8 @@ int paged_kv_append(const uint16_t *k, const uint16_t *v, const int64_t *slot_ma
 
 static int plan_with(const int32_t *tok_page_table, int max_pages, const int32_t *tok_kv_len,
                      int T, int Hq, int Hkv, int P, int d, void *workspace,
-                     size_t workspace_bytes, void *stream, int min_run);
+                     size_t workspace_bytes, void *stream, int min_run, int maps = 1,
+                     bool windowed = false, int window = INT_MAX);
 
 int paged_kv_append_fp8(const uint16_t *k, const uint16_t *v, const int64_t *slot_mapping, int T,
                         uint8_t *k8_pages, uint8_t *v8t_pages, float *k_scale, float *v_scale,
@@ -329,14 +336,15 @@ size_t paged_attn_workspace_size(int T, int Hq, int Hkv, int d) {
 
 static int plan_with(const int32_t *tok_page_table, int max_pages, const int32_t *tok_kv_len,
                      int T, int Hq, int Hkv, int P, int d, void *workspace,
-                     size_t workspace_bytes, void *stream, int min_run) {
+                     size_t workspace_bytes, void *stream, int min_run, int maps, bool windowed,
+                     int window) {
   int st = check_attn(nullptr, nullptr, nullptr, tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv,
-                      P, d, 1, nullptr, workspace, workspace_bytes, false);
+                      P, d, 1, nullptr, workspace, workspace_bytes, false, maps);
   if (st != PA_OK) return st;
   if (T == 0) return PA_OK;
   const int C = sm_count();
-  WsLayout lay = ws_layout(T, Hq, Hkv, d, C);
-  const int G = Hq / Hkv;
+  WsLayout lay = ws_layout(T, Hq * maps, Hkv, d, C);
+  const int G = Hq * maps / Hkv;
   const int NP = G >= 2 ? G / 2 : 1;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   unsigned char *ws = static_cast<unsigned char *>(workspace);
@@ -344,8 +352,8 @@ static int plan_with(const int32_t *tok_page_table, int max_pages, const int32_t
   if (blocks > 65535) blocks = 65535;
   k_plan_mark<<<blocks, 256, 0, s>>>(tok_page_table, max_pages, T, ws, lay);
   if (cudaGetLastError() != cudaSuccess) return PA_ELAUNCH;
-  k_plan<<<1, 1024, 0, s>>>(tok_page_table, max_pages, tok_kv_len, T, P, Hkv, NP, min_run, C, ws,
-                            lay);
+  k_plan<<<1, 1024, 0, s>>>(tok_page_table, max_pages, tok_kv_len, T, P, Hkv, NP, min_run, window,
+                            windowed, C, ws, lay);
   return launch_status(cudaGetLastError());
 }
 
@@ -502,6 +510,142 @@ int paged_attn_forward(const uint16_t *q, const uint16_t *k_pages, const uint16_
   if (st != PA_OK) return st;
   return paged_attn_run(q, k_pages, v_pages, tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P,
                         d, num_pages, scale, out, workspace, workspace_bytes, stream);
+}
+
+size_t paged_attn_diff_workspace_size(int T, int Hq, int Hkv, int d) {
+  if (T < 0 || check_shape(Hq, Hkv, 16, d) != PA_OK) return 0;
+  int C = sm_count();
+  if (C <= 0) C = 256;  // no device visible: as paged_attn_workspace_size
+  return ws_layout(T, Hq * kDiffMaps, Hkv, d, C).total;
+}
+
+int paged_attn_plan_diff(const int32_t *tok_page_table, int max_pages, const int32_t *tok_kv_len,
+                         int T, int Hq, int Hkv, int P, int d, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+  NvtxRange nvtx_range("paged_attn_plan_diff");
+  return plan_with(tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P, d, workspace,
+                   workspace_bytes, stream, g_min_run.load(), kDiffMaps);
+}
+
+// Prefill tiles, then decode tokens, of a planned ubatch whose arguments are in `a`.
+static int run_args(const AttnArgs &a, void *stream) {
+  AttnMaps maps;
+  int st = encode_attn_maps(a, &maps);
+  if (st != PA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = launch_status(launch_prefill(a, sm_count(), &maps, s));
+  if (st != PA_OK) return st;
+  return launch_status(launch_decode(a, sm_count(), &maps, s));
+}
+
+// A softmax scale that the kernels take: they find the maximum of the unscaled scores.
+static bool good_scale(float scale) { return scale > 0.f && scale <= FLT_MAX; }
+
+static int diff_setup(const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
+                      const int32_t *tok_page_table, int max_pages, const int32_t *tok_kv_len,
+                      int T, int Hq, int Hkv, int P, int d, int num_pages, float scale,
+                      const float *lam, const float *norm_weight, float eps, float out_scale,
+                      uint16_t *out, void *workspace, size_t workspace_bytes, AttnArgs *a) {
+  int st = check_attn(q, k_pages, v_pages, tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P, d,
+                      num_pages, out, workspace, workspace_bytes, true, kDiffMaps);
+  if (st != PA_OK || T == 0) return st;
+  if (!lam || !good_scale(scale) || (norm_weight && !(eps >= 0.f))) return PA_EINVAL;
+  *a = make_args(q, k_pages, v_pages, tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P, d,
+                 num_pages, scale, out, workspace);
+  a->lay = ws_layout(T, Hq * kDiffMaps, Hkv, d, sm_count());
+  a->lam = lam;
+  a->norm_w = norm_weight;
+  a->eps = eps;
+  a->out_scale = out_scale;
+  return PA_OK;
+}
+
+int paged_attn_diff_run(const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
+                        const int32_t *tok_page_table, int max_pages, const int32_t *tok_kv_len,
+                        int T, int Hq, int Hkv, int P, int d, int num_pages, float scale,
+                        const float *lam, const float *norm_weight, float eps, float out_scale,
+                        uint16_t *out, void *workspace, size_t workspace_bytes, void *stream) {
+  NvtxRange nvtx_range("paged_attn_diff_run");
+  AttnArgs a;
+  int st = diff_setup(q, k_pages, v_pages, tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P, d,
+                      num_pages, scale, lam, norm_weight, eps, out_scale, out, workspace,
+                      workspace_bytes, &a);
+  if (st != PA_OK || T == 0) return st;
+  return run_args(a, stream);
+}
+
+int paged_attn_diff_forward(const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
+                            const int32_t *tok_page_table, int max_pages,
+                            const int32_t *tok_kv_len, int T, int Hq, int Hkv, int P, int d,
+                            int num_pages, float scale, const float *lam,
+                            const float *norm_weight, float eps, float out_scale, uint16_t *out,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+  NvtxRange nvtx_range("paged_attn_diff_forward");
+  AttnArgs a;
+  int st = diff_setup(q, k_pages, v_pages, tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P, d,
+                      num_pages, scale, lam, norm_weight, eps, out_scale, out, workspace,
+                      workspace_bytes, &a);
+  if (st != PA_OK || T == 0) return st;
+  st = paged_attn_plan_diff(tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P, d, workspace,
+                            workspace_bytes, stream);
+  if (st != PA_OK) return st;
+  return run_args(a, stream);
+}
+
+int paged_attn_plan_window(const int32_t *tok_page_table, int max_pages,
+                           const int32_t *tok_kv_len, int T, int Hq, int Hkv, int P, int d,
+                           int window, void *workspace, size_t workspace_bytes, void *stream) {
+  NvtxRange nvtx_range("paged_attn_plan_window");
+  if (window < 1) return PA_EINVAL;
+  return plan_with(tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P, d, workspace,
+                   workspace_bytes, stream, g_min_run.load(), 1, true, window);
+}
+
+static int window_setup(const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
+                        const int32_t *tok_page_table, int max_pages, const int32_t *tok_kv_len,
+                        int T, int Hq, int Hkv, int P, int d, int num_pages, float scale,
+                        const float *sink, uint16_t *out, void *workspace, size_t workspace_bytes,
+                        AttnArgs *a) {
+  int st = check_attn(q, k_pages, v_pages, tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P, d,
+                      num_pages, out, workspace, workspace_bytes, true);
+  if (st != PA_OK || T == 0) return st;
+  if (!good_scale(scale)) return PA_EINVAL;
+  *a = make_args(q, k_pages, v_pages, tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P, d,
+                 num_pages, scale, out, workspace);
+  a->windowed = true;
+  a->sink = sink;
+  return PA_OK;
+}
+
+int paged_attn_window_run(const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
+                          const int32_t *tok_page_table, int max_pages,
+                          const int32_t *tok_kv_len, int T, int Hq, int Hkv, int P, int d,
+                          int num_pages, float scale, const float *sink, uint16_t *out,
+                          void *workspace, size_t workspace_bytes, void *stream) {
+  NvtxRange nvtx_range("paged_attn_window_run");
+  AttnArgs a;
+  int st = window_setup(q, k_pages, v_pages, tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P,
+                        d, num_pages, scale, sink, out, workspace, workspace_bytes, &a);
+  if (st != PA_OK || T == 0) return st;
+  return run_args(a, stream);
+}
+
+int paged_attn_window_forward(const uint16_t *q, const uint16_t *k_pages,
+                              const uint16_t *v_pages, const int32_t *tok_page_table,
+                              int max_pages, const int32_t *tok_kv_len, int T, int Hq, int Hkv,
+                              int P, int d, int num_pages, float scale, int window,
+                              const float *sink, uint16_t *out, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+  NvtxRange nvtx_range("paged_attn_window_forward");
+  if (window < 1) return PA_EINVAL;
+  AttnArgs a;
+  int st = window_setup(q, k_pages, v_pages, tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P,
+                        d, num_pages, scale, sink, out, workspace, workspace_bytes, &a);
+  if (st != PA_OK || T == 0) return st;
+  st = paged_attn_plan_window(tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P, d, window,
+                              workspace, workspace_bytes, stream);
+  if (st != PA_OK) return st;
+  return run_args(a, stream);
 }
 
 int paged_attn_validate(const int32_t *tok_page_table, int max_pages, const int32_t *tok_kv_len,

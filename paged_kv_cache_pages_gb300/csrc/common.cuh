@@ -14,7 +14,10 @@ namespace pa {
 // Workspace layout (device memory owned by the caller).
 //
 //   [0, 256)       WsHeader
-//   tiles          int4 [T]      (tok_start, n_tok, n_kblocks, max kv_len)
+//   tiles          int4 [T]      (tok_start, n_tok, n_kblocks, max kv_len); a windowed plan
+//                                  counts only the key blocks from the one that holds the
+//                                  tile's first visible key, and keeps that key's offset in
+//                                  its block in bits 16-31 of n_tok
 //   dec_tok        int  [T]      decode token indices
 //   tok_unit_off   int  [T + 1]  prefix sums of decode key blocks per token
 //   flags          int  [T]      plan scratch: run-start flags
@@ -40,10 +43,20 @@ struct WsHeader {
   int n_units;    // decode work units (token, kv head, 128-key block)
   int pf_work;    // prefill work units (item, 128-key block)
   int C;          // CTAs the plan was cut for (= SM count)
-  int T, Hq, Hkv, D, P, max_pages;
+  int T;
+  int kind;       // what the plan was made for (plan_kind): a run of another kind refuses it
+  int Hkv;
+  int window;     // windowed plan: positions a token attends to (INT_MAX: all)
+  int P, max_pages;
   int pad[52];
 };
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
+
+// A plan depends on the work items per tile and KV head (np) and on the window: the two
+// are checked before a kernel follows the plan's tile records.
+__host__ __device__ inline int plan_kind(int np, bool windowed) {
+  return np | (windowed ? 1 << 16 : 0);
+}
 
 constexpr int KB = 128;  // keys per block (decode unit and prefill key tile)
 // Prefill work units a tile item counts when the planner cuts the work into equal CTA

@@ -30,8 +30,20 @@
 // The launch is a programmatic dependent of the kernel before it: before waiting
 // for it, the producer asks L2 for the CTA's first blocks, and right after the
 // wait the grid releases the next launch, whose CTAs then take SMs as this grid's
-// CTAs leave them.  Two variants share the engine: MASK (per-slot sequence and
-// position mask: the unified-span baseline) and KV8 (FP8 E4M3 pages).
+// CTAs leave them.  Variants share the engine: MASK (per-slot sequence and position
+// mask: the unified-span baseline), KV8 (FP8 E4M3 pages), DIFF (differential attention)
+// and WIN (a window over the last positions, with sinks).
+//
+// DIFF: a cached K row is two keys (k1 | k2) and a query row (q1 | q2); out = norm(A1 V -
+// lam A2 V).  Rows 0-7 of the 16-row tile, the group's heads, take the first map and rows
+// 8-15, empty otherwise, the second: the k-steps of the first half of the row carry q1 in
+// rows 0-7 and those of the second half q2 in rows 8-15, so both maps' scores and both
+// weighted sums come from exactly the mma.sync instructions that one map needs (the
+// launch stays bound by its K/V bytes).  A partial holds 2 G rows; the difference and the
+// norm are taken once, where a row's parts meet.
+//
+// WIN: the plan lays out only the blocks from the one that holds a token's first visible
+// key, so the bytes before the window are never read.
 #include "kernels.cuh"
 #include "tc.cuh"
 #include "tmap.cuh"
@@ -51,9 +63,12 @@ static_assert(kKeysPerWarp == 16, "warp key slice is 16 rows");
 
 constexpr int kBarBytes = 1024;  // barriers, stage metadata, jobs, flags
 
-template <int D, int G, bool MASK, bool KV8>
+enum DecVar { kDecPlain, kDecMask, kDecKv8, kDecDiff, kDecWin };
+
+template <int D, int G, int VAR>
 struct DecCfg {
-  static_assert(!(MASK && KV8), "one variant at a time");
+  static constexpr bool MASK = VAR == kDecMask, KV8 = VAR == kDecKv8, DIFF = VAR == kDecDiff;
+  static constexpr int R = DIFF ? kDiffMaps * G : G;  // rows of a partial
   static_assert(!KV8 || D == 128, "FP8 pages: 128-byte rows");
   static constexpr int kHalves = KV8 ? 1 : D / 64;
   static constexpr int kBlk = KV8 ? KB * D : kHalves * kBox;  // one block of K (or V)
@@ -61,9 +76,11 @@ struct DecCfg {
   static constexpr int kCells = MASK ? 2 * KB * 4 : 0;        // (sequence, position) of each key
   static constexpr int kScales = KV8 ? 2 * KB * 4 : 0;        // K and V scale of each key
   static constexpr int kStage = 2 * kBlk + kQ + kCells + kScales;  // multiple of 1024
-  static constexpr int kMergeDims = 64;                       // the warps merge 64 dims at a time
-  static constexpr int kMerge = kDecWarps * G * (kMergeDims + 2) * 4;
-  static constexpr int kPart = G * (D + 2) * 4;               // one split partial (m, l, acc)
+  // the warps merge 64 dims at a time (32 for the 16 rows of the widest differential group,
+  // which leaves room for a third stage)
+  static constexpr int kMergeDims = R > 8 ? 32 : 64;
+  static constexpr int kMerge = kDecWarps * R * (kMergeDims + 2) * 4;
+  static constexpr int kPart = R * (D + 2) * 4;               // one split partial (m, l, acc)
   static constexpr int kBase = kMerge + kPart + kBarBytes;    // + own partial, barriers, jobs
   static constexpr int kBudget = 227 * 1024 - 2048;           // minus alignment slack
   static constexpr int NS0 = (kBudget - kBase) / kStage;
@@ -93,7 +110,7 @@ struct StageMeta {
   int tok;        // ubatch token
   int seg_begin;  // global unit index of the first block of (i, g)
   int seq, pos;   // masked variant: the token's sequence and position
-  int pad;
+  int lo;         // windowed variant: first visible key of the block (0 past the first one)
 };
 
 struct DecBars {
@@ -334,6 +351,42 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&h);
 }
 
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// The softmax denominator with the sink's logit (log2 units) beside the row's keys, whose sum
+// is L relative to the max M: the sink adds e^sink and no value.  A row without keys keeps its
+// sum of 0 (a zero row), an overflow to infinity is a row that the sink takes whole.
+__device__ __forceinline__ float with_sink(const float *sink, int h, float M, float L) {
+  return sink && L > 0.f ? L + exp2_approx(__ldg(sink + h) * kLog2e - M) : L;
+}
+
+// Differential attention: one warp takes the difference of the two maps' outputs of query
+// head h (already divided by their sums; lane holds dims lane + 32 j), norms and stores it.
+template <int D>
+__device__ __forceinline__ void diff_store(const AttnArgs &a, int tok, int h,
+                                           const float (&o1)[D / 32], const float (&o2)[D / 32],
+                                           int lane) {
+  const float lam = __ldg(a.lam + h);
+  float y[D / 32], ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) {
+    y[j] = __fmaf_rn(-lam, o2[j], o1[j]);
+    ss = __fmaf_rn(y[j], y[j], ss);
+  }
+  float f = a.out_scale;
+  if (a.norm_w) f *= rsqrtf(warp_sum(ss) * (1.f / D) + a.eps);
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) {
+    const int dd = lane + 32 * j;
+    const float w = a.norm_w ? __ldg(a.norm_w + dd) : 1.f;
+    a.out[((size_t)tok * a.Hq + h) * D + dd] = __half_as_ushort(__float2half_rn(y[j] * f * w));
+  }
+}
+
 // MASK: per-slot masked variant (the unified-span baseline): key j of a token is used
 // only if its slot holds a cell of the token's own sequence at a position up to the
 // token's own (cell_seq / cell_pos, copied into the stage with the block).
@@ -341,10 +394,13 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
 // (page, head) block; page size 128, d 128): the consumers widen the codes to f16
 // for the same tensor-path contractions, apply the K scales to the scores and fold
 // the V scales into P.
-template <int D, int G, bool MASK, bool KV8>
+template <int D, int G, int VAR>
 __global__ void __launch_bounds__(kDecThreads, 1)
 k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
-  using Cfg = DecCfg<D, G, MASK, KV8>;
+  using Cfg = DecCfg<D, G, VAR>;
+  constexpr bool MASK = Cfg::MASK, KV8 = Cfg::KV8, DIFF = Cfg::DIFF, WIN = VAR == kDecWin;
+  constexpr int R = Cfg::R;                // rows of a partial: the group's heads, twice if DIFF
+  constexpr int NM = DIFF ? kDiffMaps : 1;  // softmax maps per head
   constexpr int NS = Cfg::NS;
   // units asked of L2 before the dependency wait, so that the first blocks stream in
   // while the launch before drains (the depth of each variant is the measured best)
@@ -361,7 +417,7 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   DecBars *bars = reinterpret_cast<DecBars *>(smem + NS * Cfg::kStage + Cfg::kMerge);
   // this CTA's partial of its final segment, then the other CTAs' partials of it
   float *own = reinterpret_cast<float *>(smem + NS * Cfg::kStage + Cfg::kMerge + kBarBytes);
-  float *pref = own + G * (D + 2);
+  float *pref = own + R * (D + 2);
 
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   if (tid == 0) {
@@ -400,6 +456,7 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
     const int2 cnt0 =
         KV8 ? make_int2(0, 0) : ld_v2_early(&reinterpret_cast<const WsHeader *>(a.ws)->n_dec);
     const int g = s0.y, kb = s0.z, tok = s0.w, units = s1.x;
+    const int kb0 = WIN ? (s1.y + KB - 1) / KB - units : 0;  // the window's first key block
     const int ppb = KB / a.P;  // pages per key block
     // the length of the CTA's range, as the plan cuts it
     const int U0 = cnt0.y, C0 = min((int)gridDim.x, U0);
@@ -408,7 +465,8 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
                                         : 0;
     // a CTA without units has no record: only in-range rows are looked up
     const bool sane = tok >= 0 && tok < a.T && kb >= 0 && g >= 0 && g < a.Hkv && units > 0 &&
-                      kb < units;
+                      kb < units &&
+                      (!WIN || (kb0 >= 0 && (long long)(kb0 + units - 1) * ppb < a.max_pages));
     // The first kPre units of the range, continuing into the token's next heads (which
     // use the same page ids; FP8 pages: the first head's units only); all page ids are
     // requested as soon as the record is in, before the first is used, and the range
@@ -421,7 +479,8 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
     for (int u = 0; u < kPre; ++u) {
       gid[u] = gu;
       pid[u] = u == 0 ? p0.x
-                      : (u < nld && gu < a.Hkv ? __ldcg(a.tpt + (size_t)tok * a.max_pages + ku) : -1);
+                      : (u < nld && gu < a.Hkv ? __ldcg(a.tpt + (size_t)tok * a.max_pages + kb0 + ku)
+                                                   : -1);
       if (++ku >= units) {
         ku = 0;
         ++gu;
@@ -463,6 +522,15 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   // counts (every thread) and the CTA's start record with its first page ids (the
   // producer warp).
   const int2 counts = ld_v2_early(&hdr->n_dec);  // (n_dec, n_units)
+  if (DIFF || WIN) {
+    // the plan must be of this kind (its units and the workspace layout depend on it)
+    const int want = DIFF ? plan_kind(G, false) : plan_kind(G >= 2 ? G / 2 : 1, true);
+    if (__ldcg(&hdr->kind) != want) {
+      if (tid == 0 && blockIdx.x == 0) atomicOr(&hdr->err, PA_ERR_PLAN);
+      return;
+    }
+  }
+  const int window = WIN ? __ldcg(&hdr->window) : 0;
   const int4 *start = reinterpret_cast<const int4 *>(a.ws + a.lay.dec_start) + 4 * c;
   int4 start0 = make_int4(0, 0, 0, 0), start1 = start0, start2 = start0, start3 = start0;
   if (w == kDecWarps) {
@@ -518,8 +586,13 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       // producer waits for a free stage) so no global load sits on the issue path
       int pgs[8];
       int npg = 0;
+      // first key of unit u's block, and its first visible one (windowed variant)
+      auto key0_of = [&](const UnitIt &u) {
+        return WIN ? ((u.L + KB - 1) / KB - u.units + u.kb) * KB : u.kb * KB;
+      };
+      auto lo_of = [&](const UnitIt &u) { return WIN ? max(u.L - window - key0_of(u), 0) : 0; };
       auto fetch_pages = [&](const UnitIt &u) {
-        const int key0 = u.kb * KB;
+        const int key0 = key0_of(u);
         const int rows = min(KB, u.L - key0);
         npg = (rows + a.P - 1) / a.P;
         const int32_t *row = a.tpt + (size_t)u.tok * a.max_pages + key0 / a.P;
@@ -528,7 +601,7 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       };
       {  // the first unit's page ids come with its start record
         const int4 p0 = start2, p1 = start3;
-        npg = (min(KB, pit.L - pit.kb * KB) + a.P - 1) / a.P;
+        npg = (min(KB, pit.L - key0_of(pit)) + a.P - 1) / a.P;
         pgs[0] = p0.x; pgs[1] = p0.y; pgs[2] = p0.z; pgs[3] = p0.w;
         pgs[4] = p1.x; pgs[5] = p1.y; pgs[6] = p1.z; pgs[7] = p1.w;
       }
@@ -554,18 +627,20 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           if (appended <= k) break;
         }
         unsigned char *stage = ring + st * Cfg::kStage;
-        int rows = min(KB, pit.L - pit.kb * KB);
-        // every page of the block must exist, else the block is skipped (and flagged)
+        int rows = min(KB, pit.L - key0_of(pit));
+        // every page of the block must exist, else the block is skipped (and flagged); pages
+        // that lie before the window may be gone
+        const int jlo = WIN ? lo_of(pit) / a.P : 0;
         int ys[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int page = pgs[j];
-          const bool bad = j < npg && (page < 0 || page >= a.num_pages);
+          const bool bad = j < npg && j >= jlo && (page < 0 || page >= a.num_pages);
           if (bad) {
             atomicOr(err, PA_ERR_PAGE_RANGE);
             rows = 0;
           }
-          ys[j] = (j < npg && !bad) ? (page * a.Hkv + pit.g) * a.P : oob_row;
+          ys[j] = (j < npg && j >= jlo && !bad) ? (page * a.Hkv + pit.g) * a.P : oob_row;
         }
         const bool seg_first = (k == 0) || pit.kb == 0;
         {
@@ -579,6 +654,7 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           m.seg_begin = a.Hkv * pit.uoff + pit.g * pit.units;
           m.seq = pit.seq;
           m.pos = pit.pos;
+          if (WIN) m.lo = lo_of(pit);
         }
         const uint32_t qbytes = seg_first ? (uint32_t)(G * D * 2) : 0u;
         // masked variant: the (sequence, position) of each slot of the block's pages
@@ -755,15 +831,15 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           if (ok) {
             __syncwarp();  // lane 0's acquire orders every lane's reads below
             // copy in float2 steps, a batch of loads in flight per part
-            constexpr int N2 = G * (D + 2) / 2;
+            constexpr int N2 = R * (D + 2) / 2;
             constexpr int PER = (N2 + 31) / 32;
             int slot = 0;
             for (int jp = 0; jp < n_parts; ++jp) {
               const int cc = sp.c_first + jp;
               if (cc == c) continue;
               const float2 *src =
-                  reinterpret_cast<const float2 *>(partials + (size_t)(job.ig + cc) * G * (D + 2));
-              float2 *dst = reinterpret_cast<float2 *>(pref + slot * G * (D + 2));
+                  reinterpret_cast<const float2 *>(partials + (size_t)(job.ig + cc) * R * (D + 2));
+              float2 *dst = reinterpret_cast<float2 *>(pref + slot * R * (D + 2));
               float2 t[PER];
 #pragma unroll
               for (int r = 0; r < PER; ++r) {
@@ -790,6 +866,53 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         old = __shfl_sync(0xffffffffu, old, 0);
         if (old != n_parts - 1) continue;
         __syncwarp();  // lane 0's acquire orders every lane's reads below
+        if constexpr (DIFF) {
+          // the fold below for two heads at a time (their four rows fit this warp's
+          // registers), then the difference and the norm
+          constexpr int NH = G >= 2 ? 2 : 1, NE = D / 32;
+          for (int h0 = 0; h0 < G; h0 += NH) {
+            float O[2 * NH][NE], Mh[2 * NH], Lh[2 * NH];
+#pragma unroll
+            for (int x = 0; x < 2 * NH; ++x) {
+              Mh[x] = -INFINITY;
+              Lh[x] = 0.f;
+#pragma unroll
+              for (int e = 0; e < NE; ++e) O[x][e] = 0.f;
+            }
+            for (int jp = 0; jp < n_parts; ++jp) {
+              const float *base = partials + (size_t)(job.ig + sp.c_first + jp) * R * (D + 2);
+              float Op[2 * NH][NE], mp[2 * NH], lp[2 * NH];
+#pragma unroll
+              for (int x = 0; x < 2 * NH; ++x) {  // row of (map x / NH, head h0 + x % NH)
+                const float *rw = base + ((x / NH) * G + h0 + x % NH) * (D + 2);
+                mp[x] = __ldcg(rw);
+                lp[x] = __ldcg(rw + 1);
+#pragma unroll
+                for (int e = 0; e < NE; ++e) Op[x][e] = __ldcg(rw + 2 + lane + 32 * e);
+              }
+#pragma unroll
+              for (int x = 0; x < 2 * NH; ++x) {  // the arithmetic of fold_pair
+                const float Mn = fmaxf(Mh[x], mp[x]);
+                const float fo = Mh[x] == -INFINITY ? 0.f : exp2_approx(Mh[x] - Mn);
+                const float fp = mp[x] == -INFINITY ? 0.f : exp2_approx(mp[x] - Mn);
+                Lh[x] = __fmaf_rn(lp[x], fp, __fmul_rn(Lh[x], fo));
+                Mh[x] = Mn;
+#pragma unroll
+                for (int e = 0; e < NE; ++e)
+                  O[x][e] = __fmaf_rn(Op[x][e], fp, __fmul_rn(O[x][e], fo));
+              }
+            }
+#pragma unroll
+            for (int x = 0; x < 2 * NH; ++x)
+#pragma unroll
+              for (int e = 0; e < NE; ++e) O[x][e] = Lh[x] > 0.f ? O[x][e] / Lh[x] : 0.f;
+#pragma unroll
+            for (int x = 0; x < NH; ++x)
+              diff_store<D>(a, job.tok, job.g * G + h0 + x, O[x], O[NH + x], lane);
+          }
+          if (lane == 0) dec_cnt[job.ig] = 0;  // ready for the next run of this plan
+          continue;
+        }
         // Online fold over the parts in CTA order.  Lane owns outputs idx = lane + 32 t;
         // per part, lanes < G fetch (m, l) of head `lane` and broadcast the factors, and
         // every lane issues all its accumulator loads before using any (one L2 round
@@ -830,7 +953,8 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
 #pragma unroll
         for (int t = 0; t < NOUT; ++t) {
           const int idx = lane + 32 * t, h = idx / D, dd = idx - h * D;
-          const float L = __shfl_sync(0xffffffffu, Lh, h);
+          float L = __shfl_sync(0xffffffffu, Lh, h);
+          if (WIN) L = with_sink(a.sink, job.g * G + h, __shfl_sync(0xffffffffu, Mh, h), L);
           a.out[((size_t)job.tok * a.Hq + job.g * G + h) * D + dd] =
               __half_as_ushort(__float2half_rn(L > 0.f ? O[t] / L : 0.f));
         }
@@ -850,9 +974,14 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
 
   int seg_begin = 0;
   uint32_t qa[KSTEPS][2];  // A fragments of Q: columns 2cq.. and 8+2cq.. of each k-step
-  float o[NT][4];          // O accumulators (rows hr and hr + 8)
-  float m_run = -INFINITY; // running max of head hr (log2 domain)
-  float l_part = 0.f;      // this lane's share of the row sum of head hr
+  float o[NT][4];          // O accumulators (rows hr and hr + 8; DIFF: the two maps)
+  float m_run[NM];         // running max of head hr (log2 domain), per map
+  float l_part[NM];        // this lane's share of the row sum of head hr, per map
+#pragma unroll
+  for (int x = 0; x < NM; ++x) {
+    m_run[x] = -INFINITY;
+    l_part[x] = 0.f;
+  }
   int n_jobs = 0;          // jobs handed to the combining warp
   SegParts fin = {0, 0};  // parts of a split final segment
 
@@ -904,8 +1033,11 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-      m_run = -INFINITY;
-      l_part = 0.f;
+#pragma unroll
+      for (int x = 0; x < NM; ++x) {
+        m_run[x] = -INFINITY;
+        l_part[x] = 0.f;
+      }
     }
 
     const int nr = min(max(rows - key_base, 0), kKeysPerWarp);
@@ -920,6 +1052,9 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
                         cs[KB + key_base + kr] <= cit.pos;
       any_kept = __ballot_sync(0xffffffffu, keep) != 0u;
     }
+    // windowed variant: keys below `lo` of the warp's slice lie before the window
+    const int lo = WIN ? cit.lo - key_base : 0;
+    if (WIN && lo >= kKeysPerWarp) any_kept = false;
     if (nr > 0 && any_kept) {
       // ---- S = Q K^T for the warp's 16 keys (two 8-key tiles), f32 accumulators
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -944,48 +1079,62 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           const int box = ks >> 2, chunk = (ks & 3) * 2 + lm_chunk;
           uint32_t b0, b1, b2, b3;
           ldsm_x4(sK + box * kBox + sw128(lm_key, chunk), b0, b1, b2, b3);
+          if (DIFF && ks >= KSTEPS / 2) {  // the second map: q2 in rows 8-15
+            mma16816(s[0], 0u, qa[ks][0], 0u, qa[ks][1], b0, b1);
+            mma16816(s[1], 0u, qa[ks][0], 0u, qa[ks][1], b2, b3);
+            continue;
+          }
           mma16816(s[0], qa[ks][0], 0u, qa[ks][1], 0u, b0, b1);
           mma16816(s[1], qa[ks][0], 0u, qa[ks][1], 0u, b2, b3);
         }
       }
       // ---- online softmax on the fragment: this lane has keys 2cq, 2cq+1 (+8) of head hr
-      float x[4];
+      float x[NM][4];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int kk = t * 8 + 2 * cq + e;
-          bool ok = kk < nr;
+          bool ok = kk < nr && (!WIN || kk >= lo);
           if (MASK) {
             const int *cs = reinterpret_cast<const int *>(stage + 2 * Cfg::kBlk + Cfg::kQ);
             ok = ok && cs[key_base + kk] == cit.seq && cs[KB + key_base + kk] <= cit.pos;
           }
           float sv = s[t][e];
           if (KV8) sv *= reinterpret_cast<const float *>(stage + 2 * Cfg::kBlk + Cfg::kQ)[key_base + kk];
-          x[t * 2 + e] = ok ? sv * a.scale_log2 : -INFINITY;
+          x[0][t * 2 + e] = ok ? sv * a.scale_log2 : -INFINITY;
+          if constexpr (DIFF) x[1][t * 2 + e] = ok ? s[t][2 + e] * a.scale_log2 : -INFINITY;
         }
-      const float xm = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-      if (__any_sync(0xffffffffu, xm > m_run + kDecRescale)) {
-        // the running max moves: exact block max of the row (its quad), rescale
-        float bm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, 1));
-        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
-        const float m_new = fmaxf(m_run, bm);
-        const float alpha = (m_run == -INFINITY) ? 0.f : exp2_approx(m_run - m_new);
-        m_run = m_new;
-        l_part *= alpha;
+      float p[NM][4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          o[t][0] *= alpha;
-          o[t][1] *= alpha;
+      for (int r = 0; r < NM; ++r) {
+        const float xm = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
+        if (__any_sync(0xffffffffu, xm > m_run[r] + kDecRescale)) {
+          // the running max moves: exact block max of the row (its quad), rescale
+          float bm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, 1));
+          bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
+          const float m_new = fmaxf(m_run[r], bm);
+          const float alpha = (m_run[r] == -INFINITY) ? 0.f : exp2_approx(m_run[r] - m_new);
+          m_run[r] = m_new;
+          l_part[r] *= alpha;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            o[t][2 * r] *= alpha;
+            o[t][2 * r + 1] *= alpha;
+          }
         }
+        const float m_use = m_run[r] == -INFINITY ? 0.f : m_run[r];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[r][j] = exp2_approx(x[r][j] - m_use);  // -inf -> 0
+        l_part[r] += (p[r][0] + p[r][1]) + (p[r][2] + p[r][3]);
       }
-      const float m_use = m_run == -INFINITY ? 0.f : m_run;
-      float p[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = exp2_approx(x[j] - m_use);  // -inf -> 0
-      l_part += (p[0] + p[1]) + (p[2] + p[3]);
-      // P as the A fragment of the PV product (k = the warp's 16 keys; rows 8..15 zero)
-      uint32_t pa0, pa2;
+      // P as the A fragment of the PV product (k = the warp's 16 keys; rows 8..15: the
+      // second map, else zero)
+      uint32_t pa0, pa2, pa1 = 0u, pa3 = 0u;
+      if constexpr (DIFF) {
+        pa1 = pack_h2(p[1][0], p[1][1]);
+        pa3 = pack_h2(p[1][2], p[1][3]);
+      }
       if (KV8) {
         // fold each key's V scale into P (a key past the valid ones contributes 0)
         const float *vsc = reinterpret_cast<const float *>(stage + 2 * Cfg::kBlk + Cfg::kQ) + KB;
@@ -993,13 +1142,13 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int kk = (j >> 1) * 8 + 2 * cq + (j & 1);
-          pv[j] = kk < nr ? p[j] * vsc[key_base + kk] : 0.f;
+          pv[j] = kk < nr ? p[0][j] * vsc[key_base + kk] : 0.f;
         }
         pa0 = pack_h2(pv[0], pv[1]);
         pa2 = pack_h2(pv[2], pv[3]);
       } else {
-        pa0 = pack_h2(p[0], p[1]);
-        pa2 = pack_h2(p[2], p[3]);
+        pa0 = pack_h2(p[0][0], p[0][1]);
+        pa2 = pack_h2(p[0][2], p[0][3]);
       }
       // V rows past the valid keys may hold stale data or NaN: zero them (0 * NaN)
       if (nr < kKeysPerWarp) {
@@ -1021,6 +1170,15 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
               reinterpret_cast<uint4 *>(stage + Cfg::kBlk + hf * kBox + r * 128)[lane & 7] =
                   make_uint4(0, 0, 0, 0);
         }
+        __syncwarp();
+        zeroed = true;
+      }
+      if (WIN && lo > 0) {
+        // so may the V rows before the window
+        for (int r = key_base + (lane >> 3); r < key_base + lo; r += 4)
+          for (int hf = 0; hf < Cfg::kHalves; ++hf)
+            reinterpret_cast<uint4 *>(stage + Cfg::kBlk + hf * kBox + r * 128)[lane & 7] =
+                make_uint4(0, 0, 0, 0);
         __syncwarp();
         zeroed = true;
       }
@@ -1063,8 +1221,8 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           const int box = dchunk >> 3, chunk = dchunk & 7;
           uint32_t b0, b1, b2, b3;
           ldsm_x4_t(sV + box * kBox + sw128(lt_key, chunk), b0, b1, b2, b3);
-          mma16816(o[t], pa0, 0u, pa2, 0u, b0, b1);
-          mma16816(o[t + 1], pa0, 0u, pa2, 0u, b2, b3);
+          mma16816(o[t], pa0, pa1, pa2, pa3, b0, b1);
+          mma16816(o[t + 1], pa0, pa1, pa2, pa3, b2, b3);
         }
       }
     }
@@ -1079,48 +1237,59 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       // or a partial: in global memory for the combining warp (a segment that ends
       // inside the range), in shared memory for the final segment
       constexpr int MD = Cfg::kMergeDims < D ? Cfg::kMergeDims : D;
-      float *mw = merge;                  // [warps][G]
-      float *lw = mw + kDecWarps * G;     // [warps][G]
-      float *aw = lw + kDecWarps * G;     // [warps][G][MD]
-      float ls = l_part;
-      ls += __shfl_xor_sync(0xffffffffu, ls, 1);
-      ls += __shfl_xor_sync(0xffffffffu, ls, 2);
-      if (head_lane && cq == 0) {
-        mw[w * G + hr] = m_run;
-        lw[w * G + hr] = ls;
+      float *mw = merge;                  // [warps][R]
+      float *lw = mw + kDecWarps * R;     // [warps][R]
+      float *aw = lw + kDecWarps * R;     // [warps][R][MD]
+#pragma unroll
+      for (int x = 0; x < NM; ++x) {
+        float ls = l_part[x];
+        ls += __shfl_xor_sync(0xffffffffu, ls, 1);
+        ls += __shfl_xor_sync(0xffffffffu, ls, 2);
+        if (head_lane && cq == 0) {
+          mw[w * R + x * G + hr] = m_run[x];
+          lw[w * R + x * G + hr] = ls;
+        }
       }
       const int seg_units = cit.units;
       const bool direct = seg_begin >= u0 && seg_begin + seg_units <= u1;
       const bool final_split = !direct && k == n - 1;
       const int ig = cit.i * a.Hkv + cit.g;
       const int slot = ig + c;
-      float *part = final_split ? own : partials + (size_t)slot * G * (D + 2);
+      // DIFF: a whole segment's rows wait in `own` for the difference (a final segment that
+      // is split comes after every whole one)
+      float *part = final_split || (DIFF && direct) ? own : partials + (size_t)slot * R * (D + 2);
 #pragma unroll
       for (int d0 = 0; d0 < D; d0 += MD) {
         if (head_lane) {
 #pragma unroll
-          for (int t = d0 / 8; t < (d0 + MD) / 8; ++t) {
-            aw[(w * G + hr) * MD + t * 8 - d0 + 2 * cq] = o[t][0];
-            aw[(w * G + hr) * MD + t * 8 - d0 + 2 * cq + 1] = o[t][1];
-          }
+          for (int t = d0 / 8; t < (d0 + MD) / 8; ++t)
+#pragma unroll
+            for (int x = 0; x < NM; ++x) {
+              float *ar = aw + (w * R + x * G + hr) * MD + t * 8 - d0 + 2 * cq;
+              ar[0] = o[t][2 * x];
+              ar[1] = o[t][2 * x + 1];
+            }
         }
         consumers_sync();
-        for (int idx = tid; idx < G * MD; idx += kDecWarps * 32) {
+        for (int idx = tid; idx < R * MD; idx += kDecWarps * 32) {
           const int h = idx / MD, dd = d0 + (idx - h * MD);
           float M = -INFINITY;
 #pragma unroll
-          for (int xw = 0; xw < kDecWarps; ++xw) M = fmaxf(M, mw[xw * G + h]);
+          for (int xw = 0; xw < kDecWarps; ++xw) M = fmaxf(M, mw[xw * R + h]);
           float oo = 0.f, Ls = 0.f;
           if (M != -INFINITY) {
 #pragma unroll
             for (int xw = 0; xw < kDecWarps; ++xw) {
-              const float mx = mw[xw * G + h];
+              const float mx = mw[xw * R + h];
               const float f = mx == -INFINITY ? 0.f : exp2_approx(mx - M);
-              oo += f * aw[(xw * G + h) * MD + dd - d0];
-              Ls += f * lw[xw * G + h];
+              oo += f * aw[(xw * R + h) * MD + dd - d0];
+              Ls += f * lw[xw * R + h];
             }
           }
-          if (direct) {
+          if (WIN && direct) Ls = with_sink(a.sink, cit.g * G + h, M, Ls);
+          if (DIFF && direct) {
+            part[h * (D + 2) + 2 + dd] = Ls > 0.f ? oo / Ls : 0.f;
+          } else if (direct) {
             const float r = Ls > 0.f ? oo / Ls : 0.f;
             a.out[((size_t)cit.tok * a.Hq + cit.g * G + h) * D + dd] =
                 __half_as_ushort(__float2half_rn(r));
@@ -1132,6 +1301,22 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         }
         consumers_sync();  // the merge area may be rewritten
       }
+      // DIFF: a warp per head takes the difference of the two maps' rows in `own`
+      auto diff_rows = [&]() {
+        if constexpr (DIFF) {
+          for (int h = w; h < G; h += kDecWarps) {
+            float o1[D / 32], o2[D / 32];
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+              o1[j] = own[h * (D + 2) + 2 + lane + 32 * j];
+              o2[j] = own[(G + h) * (D + 2) + 2 + lane + 32 * j];
+            }
+            diff_store<D>(a, cit.tok, cit.g * G + h, o1, o2, lane);
+          }
+        }
+      };
+      // (`own` is next written behind the barrier of a later merge)
+      if (DIFF && direct) diff_rows();
       if (final_split) {
         // The CTA's final segment is split over CTAs.  The others usually finished
         // their parts long ago (the next CTA starts its range with it) and the combining
@@ -1147,8 +1332,8 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           const bool fetched = *reinterpret_cast<volatile int *>(&bars->fetch_ok) != 0;
           bool combine = fetched;
           if (!fetched) {
-            float *dst = partials + (size_t)slot * G * (D + 2);
-            for (int x = tid; x < G * (D + 2); x += kDecWarps * 32) dst[x] = own[x];
+            float *dst = partials + (size_t)slot * R * (D + 2);
+            for (int x = tid; x < R * (D + 2); x += kDecWarps * 32) dst[x] = own[x];
             consumers_sync();
             if (tid == 0) bars->last = atom_add_acq_rel(&dec_cnt[ig], 1) == fin.n - 1;
             consumers_sync();
@@ -1157,9 +1342,10 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           if (combine) {
             // thread -> pairs of output dims (one head); every load of a batch of 8
             // parts, for all of the thread's pairs, is in flight before the first fold
-            constexpr int NPAIR = G * D / 2;
+            constexpr int NPAIR = (R < 8 ? R : 8) * D / 2;  // of eight rows at a time
             constexpr int ITERS = (NPAIR + kDecWarps * 32 - 1) / (kDecWarps * 32);
             const int own_j = c - fin.c_first;
+            for (int r0 = 0; r0 < R; r0 += 8) {
             float M[ITERS], Ls[ITERS];
             float2 oo[ITERS];
 #pragma unroll
@@ -1175,8 +1361,8 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
               for (int j = 0; j < 8; ++j) {
                 const int jp = j0 + j;
                 if (jp == own_j || j >= nb) src[j] = own;
-                else if (fetched) src[j] = pref + (jp < own_j ? jp : jp - 1) * G * (D + 2);
-                else src[j] = partials + (size_t)(ig + fin.c_first + jp) * G * (D + 2);
+                else if (fetched) src[j] = pref + (jp < own_j ? jp : jp - 1) * R * (D + 2);
+                else src[j] = partials + (size_t)(ig + fin.c_first + jp) * R * (D + 2);
               }
               float mp[ITERS][8], lp[ITERS][8];
               float2 op[ITERS][8];
@@ -1188,7 +1374,7 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                   const bool local = fetched || j0 + j == own_j || j >= nb;
-                  const float *pp = src[j] + h * (D + 2);
+                  const float *pp = src[j] + (r0 + h) * (D + 2);
                   const float2 *p2 = reinterpret_cast<const float2 *>(pp + 2 + dd);
                   mp[r][j] = local ? pp[0] : __ldcg(pp);
                   lp[r][j] = local ? pp[1] : __ldcg(pp + 1);
@@ -1206,11 +1392,22 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
               const int pair = tid + r * kDecWarps * 32;
               if (pair < NPAIR) {
                 const int h = (2 * pair) / D, dd = 2 * pair - h * D;
-                const float r0 = Ls[r] > 0.f ? oo[r].x / Ls[r] : 0.f;
-                const float r1 = Ls[r] > 0.f ? oo[r].y / Ls[r] : 0.f;
-                *reinterpret_cast<__half2 *>(a.out + ((size_t)cit.tok * a.Hq + cit.g * G + h) * D +
-                                             dd) = __floats2half2_rn(r0, r1);
+                if (WIN) Ls[r] = with_sink(a.sink, cit.g * G + h, M[r], Ls[r]);
+                const float x0 = Ls[r] > 0.f ? oo[r].x / Ls[r] : 0.f;
+                const float x1 = Ls[r] > 0.f ? oo[r].y / Ls[r] : 0.f;
+                if (DIFF)  // this thread alone reads this pair of `own`
+                  *reinterpret_cast<float2 *>(own + (r0 + h) * (D + 2) + 2 + dd) =
+                      make_float2(x0, x1);
+                else
+                  *reinterpret_cast<__half2 *>(
+                      a.out + ((size_t)cit.tok * a.Hq + cit.g * G + h) * D + dd) =
+                      __floats2half2_rn(x0, x1);
               }
+            }
+            }
+            if constexpr (DIFF) {
+              consumers_sync();
+              diff_rows();
             }
             if (tid == 0) dec_cnt[ig] = 0;  // ready for the next run of this plan
           }
@@ -1243,19 +1440,19 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   }
 }
 
-template <int D, int G, bool MASK, bool KV8>
+template <int D, int G, int VAR>
 static cudaError_t launch_decode_t(const AttnArgs &a, int num_sms, const AttnMaps *maps,
                                    cudaStream_t s) {
-  using Cfg = DecCfg<D, G, MASK, KV8>;
+  using Cfg = DecCfg<D, G, VAR>;
   static PerDeviceOnce setup;
   if (setup.first()) {
     // setmaxnreg.inc can only draw on registers the block was launched with: refuse to
     // launch (rather than wait forever) if the compiled allocation does not cover the split
     cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, k_decode<D, G, MASK, KV8>);
+    cudaError_t e = cudaFuncGetAttributes(&fa, k_decode<D, G, VAR>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs * kDecThreads < kDecRegsSplitTotal) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(k_decode<D, G, MASK, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(k_decode<D, G, VAR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Cfg::kSmem);
     if (e != cudaSuccess) return e;
     setup.mark();
@@ -1270,7 +1467,7 @@ static cudaError_t launch_decode_t(const AttnArgs &a, int num_sms, const AttnMap
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_decode<D, G, MASK, KV8>, a, *maps);
+  return cudaLaunchKernelEx(&cfg, k_decode<D, G, VAR>, a, *maps);
 }
 
 cudaError_t launch_decode(const AttnArgs &a, int num_sms, const void *tmaps, cudaStream_t s) {
@@ -1279,16 +1476,18 @@ cudaError_t launch_decode(const AttnArgs &a, int num_sms, const void *tmaps, cud
   const bool masked = a.cell_seq != nullptr;
   if (a.k_scale) {  // FP8 pages: page size 128, d 128
     if (a.D != 128 || a.P != 128) return cudaErrorInvalidValue;
-    if (G == 1) return launch_decode_t<128, 1, false, true>(a, num_sms, maps, s);
-    if (G == 2) return launch_decode_t<128, 2, false, true>(a, num_sms, maps, s);
-    if (G == 4) return launch_decode_t<128, 4, false, true>(a, num_sms, maps, s);
-    if (G == 8) return launch_decode_t<128, 8, false, true>(a, num_sms, maps, s);
+    if (G == 1) return launch_decode_t<128, 1, kDecKv8>(a, num_sms, maps, s);
+    if (G == 2) return launch_decode_t<128, 2, kDecKv8>(a, num_sms, maps, s);
+    if (G == 4) return launch_decode_t<128, 4, kDecKv8>(a, num_sms, maps, s);
+    if (G == 8) return launch_decode_t<128, 8, kDecKv8>(a, num_sms, maps, s);
     return cudaErrorInvalidValue;
   }
 #define PA_DEC_CASE(DD, GG)                                                           \
   if (a.D == DD && G == GG)                                                           \
-    return masked ? launch_decode_t<DD, GG, true, false>(a, num_sms, maps, s)         \
-                  : launch_decode_t<DD, GG, false, false>(a, num_sms, maps, s);
+    return masked       ? launch_decode_t<DD, GG, kDecMask>(a, num_sms, maps, s)      \
+           : a.lam      ? launch_decode_t<DD, GG, kDecDiff>(a, num_sms, maps, s)      \
+           : a.windowed ? launch_decode_t<DD, GG, kDecWin>(a, num_sms, maps, s)       \
+                        : launch_decode_t<DD, GG, kDecPlain>(a, num_sms, maps, s);
   PA_DEC_CASE(128, 1) PA_DEC_CASE(128, 2) PA_DEC_CASE(128, 4) PA_DEC_CASE(128, 8)
   PA_DEC_CASE(64, 1) PA_DEC_CASE(64, 2) PA_DEC_CASE(64, 4) PA_DEC_CASE(64, 8)
 #undef PA_DEC_CASE

@@ -86,9 +86,12 @@ struct PfBars {
   // FP8 pages: a block's codes have landed (K, V); the V scales of the stage's block are in
   uint64_t kc_full, vc_full;
   uint64_t vs_full[kPfStages];
+  // DIFF: a warpgroup's row sums, then its sums of squares, are in shared memory
+  uint64_t xl_full[2], xs_full[2];
   uint32_t tmem_base;
   int abort;
 };
+static_assert(sizeof(PfBars) <= 256, "barrier area");
 
 // Bounded wait that also gives up as soon as another role of the CTA gave up.
 __device__ __forceinline__ bool pf_wait(uint64_t *bar, uint32_t parity, int *err,
@@ -210,6 +213,7 @@ __device__ __forceinline__ void widen_tile(const unsigned char *stg, unsigned ch
 // both come early, and so does their combine, instead of at the end of the launch.
 struct Seg {
   int tile, j;              // tile index, item within the tile
+  int kb0, lo_off;          // windowed plan: the item's first key block, its first visible key
   int kb_b, kb_e;           // key-block range of this piece
   int nkb, max_kv;          // whole item: key blocks, longest kv_len of the tile
   int tile_start, n_tok;    // tokens of the tile
@@ -224,18 +228,21 @@ struct SegCtx {
   const int4 *tiles;
   const int *tile_off;
   int Hkv, NP, G, items_per_tile;
+  int item_heads;  // query heads of an item: a pair, or one (DIFF: its two maps are the pair)
 };
 
 __device__ __forceinline__ void seg_load(Seg &s, const SegCtx &x) {
   int4 tl = x.tiles[s.tile];
   s.tile_start = tl.x;
-  s.n_tok = tl.y;
+  s.n_tok = tl.y & 0xffff;
+  s.lo_off = tl.y >> 16;
   s.nkb = tl.z;
   s.max_kv = tl.w;
   s.g = s.j / x.NP;
   const int pair = s.j - s.g * x.NP;
-  s.h0 = x.G >= 2 ? s.g * x.G + 2 * pair : s.g;
+  s.h0 = x.G >= 2 ? s.g * x.G + x.item_heads * pair : s.g;
   s.h1 = s.h0 + 1;
+  s.kb0 = (s.max_kv + KB - 1) / KB - s.nkb;
   // an item spans pf_item_units(nkb) units: its key blocks, then virtual ones (no work)
   s.item_start = (long long)x.tile_off[s.tile] + (long long)s.j * pf_item_units(s.nkb);
 }
@@ -307,7 +314,7 @@ struct PfWork {
   int C;                // CTAs the plan was cut for
 };
 
-__device__ __forceinline__ PfWork pf_work(const AttnArgs &a, int NP, int G) {
+__device__ __forceinline__ PfWork pf_work(const AttnArgs &a, int NP, int G, int item_heads = 2) {
   uint64_t wsp = reinterpret_cast<uint64_t>(a.ws);
   asm volatile("" : "+l"(wsp));
   const unsigned char *ws = reinterpret_cast<const unsigned char *>(wsp);
@@ -323,6 +330,7 @@ __device__ __forceinline__ PfWork pf_work(const AttnArgs &a, int NP, int G) {
   r.sx.Hkv = a.Hkv;
   r.sx.NP = NP;
   r.sx.G = G;
+  r.sx.item_heads = item_heads;
   r.sx.items_per_tile = a.Hkv * NP;
   r.start = reinterpret_cast<const int4 *>(ws + a.lay.pf_start)[c];
   return r;
@@ -505,10 +513,25 @@ __device__ __forceinline__ void kv8_widen_role(const AttnArgs &a, const AttnMaps
 // ([d][key]), so the binary16 V tile is K-major for the PV product.  Both widen into
 // the stage's binary16 tile (see widen_tile); the MMA issuers and the softmax then run
 // exactly as for binary16 pages.
-template <int D, bool MASK, bool KV8>
+//
+// DIFF: differential attention, out = norm(A1 V - lam A2 V) * out_scale.  An item is one
+// query head, and its two maps take the places of the pair of heads: S_i = Q_i K_i^T
+// contracts the i-th half of the 128-byte-swizzled Q and K rows (so one Q tile serves both
+// maps and S costs half the MMAs), O_i = P_i V the whole V rows.  At an item's end both
+// warpgroups read half of the columns of both accumulators (a warp may read its 32 TMEM
+// lanes of any column) and swap their row sums and sums of squares through shared memory,
+// so the difference and the norm never leave the SM.
+//
+// WIN: attention to the last `window` positions, with sinks.  The plan's items hold only
+// the key blocks from the one with the tile's first visible key (offset lo_off in it).
+enum PfVar { kPfPlain, kPfMask, kPfKv8, kPfDiff, kPfWin };
+
+template <int D, int VAR>
 __global__ void __launch_bounds__(kPfThreads, 1)
 k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
-  static_assert(!(MASK && KV8), "one variant at a time");
+  constexpr bool MASK = VAR == kPfMask, KV8 = VAR == kPfKv8;
+  constexpr bool DIFF = VAR == kPfDiff, WIN = VAR == kPfWin;
+  constexpr int kItemHeads = DIFF ? 1 : 2;
   static_assert(!KV8 || D == 128, "FP8 pages: d 128");
   using Cfg = PfCfg<D, KV8>;
   // rows of a split part's record: O[D] | m | l | 2 unused (D + 4 rows of 128 floats)
@@ -522,21 +545,26 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   int *err = &hdr->err;
   const int4 *tiles = reinterpret_cast<const int4 *>(a.ws + a.lay.tiles);
   const int G = a.Hq / a.Hkv;
-  const int NQ = G >= 2 ? 2 : 1;
-  const int NP = G >= 2 ? G / 2 : 1;
+  const int NQ = DIFF || G >= 2 ? 2 : 1;            // query tiles of an item
+  const int NP = DIFF ? G : G >= 2 ? G / 2 : 1;     // items per tile and KV head
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = hdr->C;
   const int c = blockIdx.x;
   if (c >= C) return;
+  if (hdr->kind != plan_kind(NP, WIN)) {  // the tile records are another operator's
+    if (c == 0 && tid == 0) atomicOr(err, PA_ERR_PLAN);
+    return;
+  }
+  const int window = WIN ? hdr->window : 0;
   // tiles whose tokens all have kv_len 0 own no work unit: their rows are zero
   for (int t = c; t < hdr->n_tiles; t += C) {
     const int4 tl = tiles[t];
     if (tl.z != 0) continue;
-    for (int x = tid; x < tl.y * a.Hq * (D / 8); x += blockDim.x)
+    for (int x = tid; x < (tl.y & 0xffff) * a.Hq * (D / 8); x += blockDim.x)
       reinterpret_cast<uint4 *>(a.out + (size_t)tl.x * a.Hq * D)[x] = make_uint4(0, 0, 0, 0);
   }
   {
-    const PfWork pw = pf_work(a, NP, G);
+    const PfWork pw = pf_work(a, NP, G, kItemHeads);
     if (pw.w0 >= pw.w1) return;
   }
   if (tid == 0) {
@@ -558,7 +586,9 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->p_full[i], 128);
       mbar_init(&bars->o_full[i], 1);
-      mbar_init(&bars->o_empty[i], 128);
+      mbar_init(&bars->o_empty[i], DIFF ? 256 : 128);  // DIFF: both warpgroups read both
+      mbar_init(&bars->xl_full[i], 128);
+      mbar_init(&bars->xs_full[i], 128);
     }
     bars->abort = 0;
     fence_mbar_init();
@@ -588,7 +618,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
    } else if (!KV8 && warp == kWarpTma && lane == 0) {
     // ------------------------------------------------------------ TMA producer
     {
-      const PfWork pw = pf_work(a, NP, G);
+      const PfWork pw = pf_work(a, NP, G, kItemHeads);
       const SegCtx &sx = pw.sx;
       uint32_t it = 0;
       int nitem = 0;
@@ -599,7 +629,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       // row coordinate of page j of key block kb in the pool map (past the end when
       // invalid: the box is zero-filled and nothing outside the pool is touched)
       auto ycoord = [&](int kb, int j) {
-        int page = row[kb * pages_per_block + j];
+        int page = row[((WIN ? w.kb0 : 0) + kb) * pages_per_block + j];
         if (page < 0 || page >= a.num_pages) {
           atomicOr(err, PA_ERR_PAGE_RANGE);
           return oob_row;
@@ -610,18 +640,20 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       auto load_kv = [&](int kb) -> bool {
         const int st = it % kPfStages;
         const uint32_t ph = (it / kPfStages) & 1u;
-        const int keys = min(KB, w.max_kv - kb * KB);
+        const int keys = min(KB, w.max_kv - ((WIN ? w.kb0 : 0) + kb) * KB);
         const int npg = (keys + a.P - 1) / a.P;
-        const uint32_t bytes = (uint32_t)npg * a.P * 128u * Cfg::kHalves;
+        // windowed: pages before the tile's first visible key are not looked at
+        const int j0 = WIN && kb == 0 ? w.lo_off / a.P : 0;
+        const uint32_t bytes = (uint32_t)(npg - j0) * a.P * 128u * Cfg::kHalves;
         if (!pf_wait(&bars->k_empty[st], ph ^ 1u, err, abort)) return false;
         mbar_arrive_expect_tx(&bars->k_full[st], bytes);
-        for (int j = 0; j < npg; ++j)
+        for (int j = j0; j < npg; ++j)
           for (int hf = 0; hf < Cfg::kHalves; ++hf)
             tc::tma_load_2d(smem + Cfg::kK + st * Cfg::kTile + hf * kBoxBytes + j * a.P * 128,
                             &maps.k, hf * 64, ycoord(kb, j), &bars->k_full[st]);
         if (!pf_wait(&bars->v_empty[st], ph ^ 1u, err, abort)) return false;
         mbar_arrive_expect_tx(&bars->v_full[st], bytes);
-        for (int j = 0; j < npg; ++j)
+        for (int j = j0; j < npg; ++j)
           for (int hf = 0; hf < Cfg::kHalves; ++hf)
             tc::tma_load_2d(smem + Cfg::kV + st * Cfg::kTile + hf * kBoxBytes + j * a.P * 128,
                             &maps.v, hf * 64, ycoord(kb, j), &bars->v_full[st]);
@@ -637,11 +669,11 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           if (!load_kv(kb++)) break;
           if (!pf_wait(&bars->q_empty, (nitem - 1) & 1, err, abort)) break;
         }
-        mbar_arrive_expect_tx(&bars->q_full, NQ * Cfg::kTile);
+        mbar_arrive_expect_tx(&bars->q_full, (DIFF ? 1 : NQ) * Cfg::kTile);
         for (int hf = 0; hf < Cfg::kHalves; ++hf) {
           tc::tma_load_3d(smem + Cfg::kQ0 + hf * kBoxBytes, &maps.q, hf * 64, w.h0, w.tile_start,
                           &bars->q_full);
-          if (NQ == 2)
+          if (!DIFF && NQ == 2)
             tc::tma_load_3d(smem + Cfg::kQ1 + hf * kBoxBytes, &maps.q, hf * 64, w.h1,
                             w.tile_start, &bars->q_full);
         }
@@ -650,7 +682,8 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           if (seg_next(nx, sx))
             for (int hf = 0; hf < Cfg::kHalves; ++hf) {
               tc::tma_prefetch_3d(&maps.q, hf * 64, nx.h0, nx.tile_start);
-              if (NQ == 2) tc::tma_prefetch_3d(&maps.q, hf * 64, nx.h1, nx.tile_start);
+              if (!DIFF && NQ == 2)
+                tc::tma_prefetch_3d(&maps.q, hf * 64, nx.h1, nx.tile_start);
             }
         }
         bool ok = true;
@@ -665,7 +698,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
     // One thread per query tile: warp 9 issues tile 0's MMAs, warp 10 tile 1's.  Each
     // thread's waits then leave the tensor pipe to the other thread's MMAs.
     const int qi = warp - kWarpMma;
-    const PfWork pw = pf_work(a, NP, G);
+    const PfWork pw = pf_work(a, NP, G, kItemHeads);
     const SegCtx &sx = pw.sx;
     constexpr uint32_t idS = tc::idesc_f16(128, 128, false);
     // V: MN-major ([key][d] rows) for binary16 pages; K-major ([d][key] rows) for FP8
@@ -685,6 +718,16 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
                    lV1 = tc::sdesc_lo(sV + Cfg::kTile, KV8 ? 16 : kBoxBytes);
     auto issue_S = [&](int i, int st) {
       const uint32_t d = tmem + i * 128;
+      if constexpr (DIFF) {
+        // map i: the i-th half of the Q and K rows (a 64-column box at d = 128, 64 bytes of
+        // the rows at d = 64: a k-step of 32 bytes never crosses a box)
+        const uint32_t m16 = i ? (D == 128 ? kBoxBytes : 64) >> 4 : 0u;
+        const uint32_t a0 = tc::opaque(lQ0 + m16), b0 = tc::opaque((st ? lK1 : lK0) + m16);
+        tc::mma_ss_lo<0>(d, a0, b0, idS);
+#pragma unroll
+        for (int kk = 1; kk < D / 32; ++kk) tc::mma_ss_lo<1>(d, a0 + 2 * kk, b0 + 2 * kk, idS);
+        return;
+      }
       const uint32_t a0 = tc::opaque(i ? lQ1 : lQ0), b0 = tc::opaque(st ? lK1 : lK0);
       tc::mma_ss_lo<0>(d, a0, b0, idS);
 #pragma unroll
@@ -694,10 +737,17 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       }
     };
     // O_i (+)= P_i V over the first nk 16-key steps of the block
-    auto issue_PV = [&](int i, int st, bool acc, int nk) {
+    // (WIN: from step k0 on, which the caller keeps below nk)
+    auto issue_PV = [&](int i, int st, bool acc, int nk, int k0) {
       const uint32_t d = tmem + 256 + i * D;
       const uint32_t p = tmem + i * 128;
       const uint32_t b0 = tc::opaque(st ? lV1 : lV0);
+      if (WIN && k0 > 0) {
+        for (int kk = k0; kk < nk; ++kk)
+          tc::mma_ts_lo_pred(d, p + kk * 8, b0 + (uint32_t)((kk * 2048) >> 4), idPV,
+                             acc || kk > k0 ? 1u : 0u);
+        return;
+      }
       tc::mma_ts_lo_pred(d, p, b0, idPV, acc ? 1u : 0u);
 #pragma unroll
       for (int kk = 1; kk < KB / 16; ++kk) {
@@ -732,8 +782,21 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         // Rows are 128 B, so whole rows are zeroed and the swizzle inside a row does not
         // matter.  Tile 0's issuer zeroes before its PV; tile 1's issues its PV only after
         // tile 0's turn, which ends after the zeroing.
-        int nk = KB / 16;
-        const int nvalid = w.max_kv - kb * KB;
+        int nk = KB / 16, k0 = 0;
+        const int nvalid = w.max_kv - ((WIN ? w.kb0 : 0) + kb) * KB;
+        if (WIN && kb == 0 && w.lo_off > 0) {
+          // the tile's first visible key: the product starts at its 16-key step, and that
+          // step's rows before it are zeroed (they may hold anything)
+          k0 = w.lo_off / 16;
+          if (qi == 0 && w.lo_off % 16) {
+            for (int hf = 0; hf < Cfg::kHalves; ++hf) {
+              uint4 *base = reinterpret_cast<uint4 *>(smem + Cfg::kV + st * Cfg::kTile +
+                                                      hf * kBoxBytes + k0 * 16 * 128);
+              for (int x = 0; x < (w.lo_off % 16) * 8; ++x) base[x] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async();
+          }
+        }
         if (kb + 1 == w.nkb && nvalid < KB) {
           nk = (nvalid + 15) / 16;
           const int n16 = (nk * 16 - nvalid) * 8;
@@ -769,7 +832,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           break;
         }
         tc::fence_after_sync();
-        issue_PV(qi, st, kk > 0, nk);
+        issue_PV(qi, st, kk > 0, nk, k0);
         if (last) tc::commit(&bars->o_full[qi]);
         tc::commit(&bars->v_empty[st]);
         if (!last) {
@@ -796,20 +859,21 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
     const uint32_t tS = tmem + wg * 128 + lane_off;
     const uint32_t tO = tmem + 256 + wg * D + lane_off;
     if (wg < NQ) {
-      const PfWork pw = pf_work(a, NP, G);
+      const PfWork pw = pf_work(a, NP, G, kItemHeads);
       const SegCtx &sx = pw.sx;
       const long long W = pw.W, w0 = pw.w0;
       const int C = pw.C;
       uint32_t sc = 0;
-      int nitem = 0;
+      int nitem = 0, nwhole = 0;
       float *parts = reinterpret_cast<float *>(a.ws + a.lay.partials);
       int *cnt = reinterpret_cast<int *>(a.ws + a.lay.pf_cnt);
       Seg w;
       for (bool more = seg_first(w, sx, pw); more; more = seg_next(w, sx)) {
-        const int h = wg ? w.h1 : w.h0;
+        const int h = !DIFF && wg ? w.h1 : w.h0;
         const int tok = w.tile_start + row;
         const bool valid = row < w.n_tok;
         const int L = valid ? min(max(a.kv[tok], 0), cap) : 0;
+        const int lo = WIN ? max(L - window, 0) : 0;  // first visible key
         // masked variant: this row's (sequence, position); -2 matches no cell
         const int my_seq = MASK && valid ? a.tok_seq[tok] : -2;
         const int my_pos = MASK && valid ? a.tok_pos[tok] : -1;
@@ -845,8 +909,10 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           if (MASK && kk + 1 < nseg) nxt_cell = cell_of(kb + 1);  // loads in flight meanwhile
           if (!pf_wait(&bars->s_full[wg], (sc + kk) & 1u, err, abort)) { ok = false; break; }
           tc::fence_after_sync();
-          const int nv = min(max(L - kb * KB, 0), KB);  // valid keys of this row here
-          const bool wfull = !MASK && __all_sync(0xffffffffu, nv == KB);
+          const int key0 = ((WIN ? w.kb0 : 0) + kb) * KB;
+          const int nv = min(max(L - key0, 0), KB);  // valid keys of this row here
+          const int nlo = WIN ? lo - key0 : 0;       // those before nlo lie before the window
+          const bool wfull = !MASK && __all_sync(0xffffffffu, nv == KB && nlo <= 0);
           const int2 *cb = reinterpret_cast<const int2 *>(smem + Cfg::kCinfo) +
                            (wg * 2 + ((sc + kk) & 1u)) * 128;
           if (MASK) {
@@ -884,7 +950,8 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
               t[j] = (mw[j >> 5] >> (j & 31)) & 1u ? t[j] : 0xff800000u;
           } else if (!wfull) {
 #pragma unroll
-            for (int j = 0; j < 128; ++j) t[j] = j < nv ? t[j] : 0xff800000u;  // -inf
+            for (int j = 0; j < 128; ++j)
+              t[j] = j < nv && (!WIN || j >= nlo) ? t[j] : 0xff800000u;  // -inf
           }
           float mx = -INFINITY;
 #pragma unroll
@@ -965,10 +1032,82 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         }
         if (!ok) break;
         if (!pf_wait(&bars->o_full[wg], nitem & 1, err, abort)) break;
+        // DIFF: y (the row's D values, or the warpgroup's half of them) times the norm's factor
+        // and weights
+        auto diff_scale = [&](float ss) {
+          return a.norm_w ? a.out_scale * rsqrtf(ss * (1.f / D) + a.eps) : a.out_scale;
+        };
+        auto diff_pack = [&](float y0, float y1, int e, float f) {
+          float2 wv = make_float2(1.f, 1.f);
+          if (a.norm_w) wv = make_float2(__ldg(a.norm_w + e), __ldg(a.norm_w + e + 1));
+          const __half2 hv = __floats2half2_rn(y0 * f * wv.x, y1 * f * wv.y);
+          return *reinterpret_cast<const uint32_t *>(&hv);
+        };
+        if (DIFF && w.kb_b == 0 && w.kb_e == w.nkb) {
+          // The whole item.  This warpgroup finishes columns [wg D/2, wg D/2 + D/2) of every
+          // row: it needs the other map's accumulator and row sum.  A buffer of the swap is
+          // rewritten only after the other warpgroup has freed the item's accumulators, which
+          // it does after it has read it.
+          constexpr int HD = D / 2;
+          float *lx = reinterpret_cast<float *>(smem + Cfg::kCinfo);  // [2][128] row sums
+          float *sq = lx + 256;                                       // [2][128] sums of squares
+          lx[wg * 128 + row] = l_run;
+          mbar_arrive(&bars->xl_full[wg]);
+          if (!pf_wait(&bars->o_full[wg ^ 1], nitem & 1, err, abort)) break;
+          if (!pf_wait(&bars->xl_full[wg ^ 1], nwhole & 1, err, abort)) break;
+          tc::fence_after_sync();
+          const float l0 = lx[row], l1 = lx[128 + row];
+          const float i0 = l0 > 0.f ? 1.f / l0 : 0.f;
+          const float i1 = l1 > 0.f ? -__ldg(a.lam + h) / l1 : 0.f;
+          const uint32_t tY = tmem + 256 + wg * HD + lane_off;
+          uint32_t o0[HD], o1[HD];
+#pragma unroll
+          for (int ch = 0; ch < HD / 32; ++ch) {
+            tc::ld32(tY + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(o0 + ch * 32));
+            tc::ld32(tY + D + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(o1 + ch * 32));
+          }
+          tc::wait_ld();
+          tc::fence_before_sync();
+          mbar_arrive(&bars->o_empty[0]);
+          mbar_arrive(&bars->o_empty[1]);
+          float y[HD], ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < HD; ++e) {
+            y[e] = __fmaf_rn(__uint_as_float(o1[e]), i1, __uint_as_float(o0[e]) * i0);
+            ss = __fmaf_rn(y[e], y[e], ss);
+          }
+          if (a.norm_w) {
+            sq[wg * 128 + row] = ss;
+            mbar_arrive(&bars->xs_full[wg]);
+            if (!pf_wait(&bars->xs_full[wg ^ 1], nwhole & 1, err, abort)) break;
+            ss = sq[row] + sq[128 + row];  // the same order in both warpgroups
+          }
+          const float f = diff_scale(ss);
+          if (valid) {
+#pragma unroll
+            for (int q = 0; q < HD / 8; ++q) {
+              uint32_t hw[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                hw[e] = diff_pack(y[q * 8 + 2 * e], y[q * 8 + 2 * e + 1], wg * HD + q * 8 + 2 * e, f);
+              orow[wg * (HD / 8) + q] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+            }
+          }
+          ++nwhole;
+          sc += nseg;
+          ++nitem;
+          continue;
+        }
         tc::fence_after_sync();
+        // the sink's share of the denominator, beside the row's keys
+        const float sink2 = WIN && a.sink ? __ldg(a.sink + h) * kLog2e : 0.f;
+        auto row_inv = [&](float m, float l) {
+          if (WIN && a.sink) return l > 0.f ? 1.f / (l + exp2_approx(sink2 - m)) : 0.f;
+          return l > 0.f ? 1.f / l : 0.f;
+        };
         if (w.kb_b == 0 && w.kb_e == w.nkb) {
           // the whole item: normalise and store f16
-          const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+          const float inv = row_inv(m_run, l_run);
           uint32_t o[D];  // the whole O row in one TMEM round trip
 #pragma unroll
           for (int ch = 0; ch < D / 32; ++ch)
@@ -1010,6 +1149,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           rec[(D + 1) * 128] = l_run;
           tc::fence_before_sync();
           mbar_arrive(&bars->o_empty[wg]);
+          if (DIFF) mbar_arrive(&bars->o_empty[wg ^ 1]);  // this warpgroup does not read it
           // count the parts that have landed; the last one combines (no waiting)
           const long long item_end = w.item_start + w.nkb;
           const int c1 = cta_of_unit(w.item_start, W, C), c2 = cta_of_unit(item_end - 1, W, C);
@@ -1017,13 +1157,69 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           for (int cc = c1; cc <= c2; ++cc) n_parts += cta_has_units(cc, W, C) ? 1 : 0;
           // one counter per (item, warpgroup, warp): a warp's 32 rows only need the same
           // 32 rows of the other parts, so warps decide independently (no cross-warp wait)
-          int *my_cnt = &cnt[((w.tile * sx.items_per_tile + w.j) * 2 + wg) * 4 + wl];
+          // (DIFF: one per (item, warp), counting both maps' parts)
+          int *my_cnt =
+              &cnt[((w.tile * sx.items_per_tile + w.j) * 2 + (DIFF ? 0 : wg)) * 4 + wl];
           __threadfence();
           __syncwarp();
           int old = 0;
           if (lane == 0) old = atomicAdd(my_cnt, 1);
           old = __shfl_sync(0xffffffffu, old, 0);
-          if (old == n_parts - 1) {
+          if (DIFF && old == 2 * n_parts - 1) {
+            // Both maps of all parts have landed: y = sum over parts of c0 O_0 - c1 O_1 with
+            // c_i = 2^(m_i - M_i) / L_i (lam in c1), one record chunk after the other.
+            __threadfence();
+            auto rec_of = [&](int cc, int map) {
+              const int sl = 2 * cc + (w.item_start <= (long long)cc * W / C ? 0 : 1);
+              return parts + ((size_t)sl * 2 + map) * (size_t)kPartStride * 128 + row;
+            };
+            float M[2] = {-INFINITY, -INFINITY}, Ls[2] = {0.f, 0.f};
+            for (int cc = c1; cc <= c2; ++cc) {
+              if (!cta_has_units(cc, W, C)) continue;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float *r = rec_of(cc, i);
+                const float mp = __ldcg(r + D * 128), lp = __ldcg(r + (D + 1) * 128);
+                const float Mn = fmaxf(M[i], mp);
+                const float fo = M[i] == -INFINITY ? 0.f : exp2_approx(M[i] - Mn);
+                const float fp = mp == -INFINITY ? 0.f : exp2_approx(mp - Mn);
+                Ls[i] = __fmaf_rn(lp, fp, __fmul_rn(Ls[i], fo));
+                M[i] = Mn;
+              }
+            }
+            const float i0 = Ls[0] > 0.f ? 1.f / Ls[0] : 0.f;
+            const float i1 = Ls[1] > 0.f ? -__ldg(a.lam + h) / Ls[1] : 0.f;
+            float y[D];
+#pragma unroll
+            for (int e = 0; e < D; ++e) y[e] = 0.f;
+            for (int cc = c1; cc <= c2; ++cc) {
+              if (!cta_has_units(cc, W, C)) continue;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float *r = rec_of(cc, i);
+                const float mp = __ldcg(r + D * 128);
+                const float cf = mp == -INFINITY ? 0.f : exp2_approx(mp - M[i]) * (i ? i1 : i0);
+#pragma unroll
+                for (int e = 0; e < D; ++e) y[e] = __fmaf_rn(__ldcg(r + e * 128), cf, y[e]);
+              }
+            }
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < D; ++e) ss = __fmaf_rn(y[e], y[e], ss);
+            const float f = diff_scale(ss);
+            if (valid) {
+#pragma unroll
+              for (int q = 0; q < D / 8; ++q) {
+                uint32_t hw[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  hw[e] = diff_pack(y[q * 8 + 2 * e], y[q * 8 + 2 * e + 1], q * 8 + 2 * e, f);
+                orow[q] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+              }
+            }
+            if (lane == 0) *my_cnt = 0;  // ready for the next run of this plan
+          }
+          if (!DIFF && old == n_parts - 1) {
             __threadfence();
             // Parts are folded in CTA order with the same arithmetic whichever CTA
             // combines, so results are reproducible.  The other parts were written by
@@ -1070,7 +1266,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
                 fk[k] = (mk[k] == -INFINITY) ? 0.f : exp2_approx(mk[k] - M);
                 if (k < np) Ls += (mk[k] == -INFINITY) ? 0.f : lk[k] * fk[k];
               }
-              const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+              const float inv = row_inv(M, Ls);
               float vb[2][kFastParts][16];
               auto load_chunk = [&](int ch, float (&v)[kFastParts][16]) {
 #pragma unroll
@@ -1110,7 +1306,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
                 const float l_p = cc == c ? l_run : __ldcg(r + (D + 1) * 128);
                 Ls += (m_p == -INFINITY) ? 0.f : l_p * exp2_approx(m_p - M);
               }
-              const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+              const float inv = row_inv(M, Ls);
 #pragma unroll
               for (int ch = 0; ch < D / 16; ++ch) {
                 float acc[16];
@@ -1159,24 +1355,24 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   }
 }
 
-template <int D, bool MASK, bool KV8>
+template <int D, int VAR>
 static cudaError_t launch_prefill_t(const AttnArgs &a, int num_sms, const AttnMaps *maps,
                                     cudaStream_t s) {
-  using Cfg = PfCfg<D, KV8>;
+  using Cfg = PfCfg<D, VAR == kPfKv8>;
   static PerDeviceOnce setup;
   if (setup.first()) {
     // setmaxnreg.inc can only draw on registers the block was launched with: refuse to
     // launch (rather than wait forever) if the compiled allocation does not cover the split
     cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, k_prefill<D, MASK, KV8>);
+    cudaError_t e = cudaFuncGetAttributes(&fa, k_prefill<D, VAR>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs * kPfThreads < kRegsSplitTotal) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(k_prefill<D, MASK, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(k_prefill<D, VAR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Cfg::kSmem);
     if (e != cudaSuccess) return e;
     setup.mark();
   }
-  k_prefill<D, MASK, KV8><<<num_sms, kPfThreads, Cfg::kSmem, s>>>(a, *maps);
+  k_prefill<D, VAR><<<num_sms, kPfThreads, Cfg::kSmem, s>>>(a, *maps);
   return cudaGetLastError();
 }
 
@@ -1185,12 +1381,17 @@ cudaError_t launch_prefill(const AttnArgs &a, int num_sms, const void *tmaps, cu
   const bool mask = a.cell_seq != nullptr;
   if (a.k_scale) {  // FP8 pages: page size 128, d 128
     if (a.D != 128 || a.P != KB || mask) return cudaErrorInvalidValue;
-    return launch_prefill_t<128, false, true>(a, num_sms, maps, s);
+    return launch_prefill_t<128, kPfKv8>(a, num_sms, maps, s);
   }
-  if (a.D == 128) return mask ? launch_prefill_t<128, true, false>(a, num_sms, maps, s)
-                              : launch_prefill_t<128, false, false>(a, num_sms, maps, s);
-  if (a.D == 64) return mask ? launch_prefill_t<64, true, false>(a, num_sms, maps, s)
-                             : launch_prefill_t<64, false, false>(a, num_sms, maps, s);
+#define PA_PF_CASE(DD)                                                        \
+  if (a.D == DD)                                                              \
+    return mask         ? launch_prefill_t<DD, kPfMask>(a, num_sms, maps, s)  \
+           : a.lam      ? launch_prefill_t<DD, kPfDiff>(a, num_sms, maps, s)  \
+           : a.windowed ? launch_prefill_t<DD, kPfWin>(a, num_sms, maps, s)   \
+                        : launch_prefill_t<DD, kPfPlain>(a, num_sms, maps, s);
+  PA_PF_CASE(128)
+  PA_PF_CASE(64)
+#undef PA_PF_CASE
   return cudaErrorInvalidValue;
 }
 

@@ -6,6 +6,8 @@
 //   k_validate table check without trapping
 //   k_plan     one-CTA device planner: same-row runs -> tensor-core tiles,
 //              short runs -> split-KV decode work
+#include <climits>
+
 #include "kernels.cuh"
 
 namespace pa {
@@ -245,7 +247,8 @@ __device__ __forceinline__ int upper_index(const int *off, int n, long long u, l
 
 __global__ void __launch_bounds__(kPlanThreads, 1)
 k_plan(const int32_t *__restrict__ tpt, int max_pages, const int32_t *__restrict__ kv, int T,
-       int P, int Hkv, int NP, int min_run, int C, unsigned char *ws, WsLayout lay) {
+       int P, int Hkv, int NP, int min_run, int window, bool windowed, int C, unsigned char *ws,
+       WsLayout lay) {
   __shared__ int sh[32];
   WsHeader *hdr = reinterpret_cast<WsHeader *>(ws);
   int4 *tiles = reinterpret_cast<int4 *>(ws + lay.tiles);
@@ -305,21 +308,29 @@ k_plan(const int32_t *__restrict__ tpt, int max_pages, const int32_t *__restrict
   for (int i = tid; i < tile_base * Hkv * NP * 8; i += kPlanThreads) pf_cnt[i] = 0;
   for (int i = tid; i < dec_base * Hkv; i += kPlanThreads) dec_cnt[i] = 0;
 
-  // 3. key blocks of each tile: ceil(max kv_len over its tokens / 128); one warp per tile
+  // 3. key blocks of each tile: ceil(max kv_len over its tokens / 128), less the blocks that
+  // lie before every token's window; one warp per tile
   for (int i = warp; i < tile_base; i += kPlanThreads / 32) {
     int4 tl = tiles[i];
-    int mx = 0;
+    int mx = 0, lo = INT_MAX;
     bool bad = false;
     for (int u = tl.x + lane; u < tl.x + tl.y; u += 32) {
       int L = kv[u];
       bad |= (L < 0 || L > cap);
-      mx = max(mx, min(max(L, 0), cap));
+      L = min(max(L, 0), cap);
+      mx = max(mx, L);
+      if (L > 0) lo = min(lo, max(0, L - window));
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int o = 16; o > 0; o >>= 1) {
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&hdr->err, PA_ERR_KV_RANGE);
     if (lane == 0) {
-      tiles[i].z = (mx + KB - 1) / KB;
+      if (mx == 0) lo = 0;
+      tiles[i].y = tl.y | (lo % KB) << 16;
+      tiles[i].z = (mx + KB - 1) / KB - lo / KB;
       tiles[i].w = mx;
     }
   }
@@ -346,7 +357,7 @@ k_plan(const int32_t *__restrict__ tpt, int max_pages, const int32_t *__restrict
     if (i < dec_base) {
       int L = kv[dec_tok[i]];
       if (L < 0 || L > cap) { atomicOr(&hdr->err, PA_ERR_KV_RANGE); L = L < 0 ? 0 : cap; }
-      units = (L + KB - 1) / KB;
+      units = (L + KB - 1) / KB - max(0, L - window) / KB;
     }
     int tot;
     int off = block_excl_scan(units, &tot, sh) + unit_base;
@@ -379,7 +390,8 @@ k_plan(const int32_t *__restrict__ tpt, int max_pages, const int32_t *__restrict
       dec_start[4 * c + 1] = make_int4(units, L, tok_unit_off[i], 0);
       // page ids of the first key block, so the first copy needs no table lookup
       int pg[8];
-      const int key0 = kb * KB, npg = (min(KB, L - key0) + P - 1) / P;
+      const int key0 = ((L + KB - 1) / KB - units + kb) * KB;
+      const int npg = (min(KB, L - key0) + P - 1) / P;
       const int32_t *row = tpt + (size_t)tok * max_pages + key0 / P;
       for (int j = 0; j < 8; ++j) pg[j] = j < npg ? row[j] : -1;
       dec_start[4 * c + 2] = make_int4(pg[0], pg[1], pg[2], pg[3]);
@@ -414,7 +426,9 @@ k_plan(const int32_t *__restrict__ tpt, int max_pages, const int32_t *__restrict
     hdr->pf_work = work_base;
     hdr->C = C;
     hdr->T = T;
+    hdr->kind = plan_kind(NP, windowed);
     hdr->Hkv = Hkv;
+    hdr->window = window;
     hdr->P = P;
     hdr->max_pages = max_pages;
   }

@@ -22,7 +22,8 @@ __global__ void k_validate(const int32_t *tpt, int max_pages, const int32_t *kv,
 __global__ void k_plan_mark(const int32_t *tpt, int max_pages, int T, unsigned char *ws,
                             WsLayout lay);
 __global__ void k_plan(const int32_t *tpt, int max_pages, const int32_t *kv, int T, int P, int Hkv,
-                       int NP, int min_run, int C, unsigned char *ws, WsLayout lay);
+                       int NP, int min_run, int window, bool windowed, int C, unsigned char *ws,
+                       WsLayout lay);
 
 // Per-device flags of a kernel's one-time launch setup (function attributes are per
 // device).  Returns true for the first caller on the current device, which then
@@ -65,7 +66,20 @@ struct AttnArgs {
   // [T][Hkv][d] and their slots
   const uint16_t *k_new, *v_new;
   const int64_t *slot;
+  // differential attention only, else lam is null: the weight of the second map of every
+  // query head [Hq], the norm's weight [d] (null: no norm) and its epsilon, and the factor of
+  // the output
+  const float *lam, *norm_w;
+  float eps, out_scale;
+  // windowed attention only: runs on a windowed plan, which holds the window; the sink's
+  // logit of every query head [Hq] (null: none)
+  bool windowed;
+  const float *sink;
 };
+
+// Differential attention reads a cached K row as two keys (k1 | k2) of d / 2 and a query row
+// as (q1 | q2).  For the plan and the workspace a query head counts as two, one per map.
+constexpr int kDiffMaps = 2;
 
 // Arguments of the batch build (passed by value); see paged_batch_build.
 constexpr int kBatchMaxSeq = 16384;  // two sums per request in one CTA's shared memory
