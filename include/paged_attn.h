@@ -131,7 +131,7 @@ int paged_expand_ubatch(const int32_t *seq_page_table, int n_seq, int max_pages,
  *   seq_len [n_seq] int32   cached positions of each request
  *   new_len [n_seq] int32   positions that the step adds: 0 none, 1 a decoding request, more
  *       a chunk of a prompt; < 0: the request has finished
- *   page_ref [num_pages] int32 (in/out, 16-byte aligned)  reference count of every page
+ *   page_ref [num_pages] int32 (in/out, 16-byte aligned)  reference count (>= 0) of every page
  *   q_start [n_seq + 1] int32 (out)   first token of each request; q_start[n_seq] is the
  *       number of tokens of the step
  *   seq_len_out [n_seq] int32 (out)   seq_len plus the admitted new positions (0 for a
@@ -143,8 +143,8 @@ int paged_expand_ubatch(const int32_t *seq_page_table, int n_seq, int max_pages,
  *
  * In this order:
  *   1. every page in a finished request's row loses one reference and the row becomes -1
- *      (a page that is free already: PA_ERR_REFCOUNT; an id outside the pool:
- *      PA_ERR_PAGE_RANGE; neither is counted);
+ *      (a page that is free already stays free: PA_ERR_REFCOUNT; an id outside the pool is
+ *      passed over: PA_ERR_PAGE_RANGE);
  *   2. a request with seq_len < 0, or with seq_len + new_len past its row, adds nothing
  *      (PA_ERR_SEQ_RANGE);
  *   3. the requests are admitted in order up to the first whose new pages exceed the free
@@ -153,7 +153,7 @@ int paged_expand_ubatch(const int32_t *seq_page_table, int n_seq, int max_pages,
  *   4. an admitted request's new pages (those of its positions past ceil(seq_len / P) * P)
  *      are taken with reference count 1 and written behind its last entry.
  * A request must own its last, partly filled page (pa_pool_fork).  The arrays must not
- * overlap, but for seq_len_out.  n_seq <= 16384 (else PA_EUNSUPPORTED).  Two launches.
+ * overlap, but for seq_len_out.  n_seq <= 8192 (else PA_EUNSUPPORTED).  Two launches.
  */
 int paged_batch_build(int32_t *seq_page_table, int n_seq, int max_pages, const int32_t *seq_len,
                       const int32_t *new_len, int32_t *page_ref, int num_pages, int P, int T,

@@ -25,7 +25,6 @@ Entry points mirror include/paged_attn.h:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import NamedTuple
@@ -138,26 +137,35 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _raw_stream(stream, device):
+    """The stream's handle; the device's current stream without building its Python object
+    (3 us of a call)."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None \
+        else stream.cuda_stream
+
+
 def _req(t, dtype, name):
     if not (t.is_cuda and t.dtype == dtype and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
 
 
 def _req_on(t, dtype, shape, device, name):
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device \
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device \
             or device.type != "cuda":
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
                          "one CUDA device")
 
 
-def _on(t):
-    """The tensor's device as the current one while a call is made (launches, the SM count
-    and the default stream go by the current device)."""
-    return _HERE_ALREADY if t.device.index == torch.cuda.current_device() \
-        else torch.cuda.device(t.device)
-
-
-_HERE_ALREADY = contextlib.nullcontext()
+def _call(fn_name, fn, device, args):
+    """fn(*args, the device's current stream) with `device` as the current one (launches and
+    the SM count go by it)."""
+    if device.index == torch.cuda.current_device():
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status != PA_OK:
+        raise PagedAttnError(status, fn_name)
 
 
 def workspace_size(T: int, Hq: int, Hkv: int, d: int) -> int:
@@ -219,24 +227,30 @@ def batch_build(seq_page_table, seq_len, new_len, page_ref, P, T, out=None, err=
     the free pages is admitted, and its tokens' lists are written.  seq_page_table and
     page_ref are updated in place."""
     n_seq, max_pages = seq_page_table.shape
-    for t, shape, n in ((seq_page_table, (n_seq, max_pages), "seq_page_table"),
-                        (seq_len, (n_seq,), "seq_len"), (new_len, (n_seq,), "new_len"),
-                        (page_ref, (page_ref.numel(),), "page_ref")):
-        _req_on(t, torch.int32, shape, seq_page_table.device, n)
+    dev, i32, num_pages = seq_page_table.device, torch.int32, page_ref.numel()
+    _req_on(seq_page_table, i32, (n_seq, max_pages), dev, "seq_page_table")
+    _req_on(seq_len, i32, (n_seq,), dev, "seq_len")
+    _req_on(new_len, i32, (n_seq,), dev, "new_len")
+    _req_on(page_ref, i32, (num_pages,), dev, "page_ref")
     if out is None:
-        out = new_batch(n_seq, max_pages, T, seq_page_table.device)
+        out = new_batch(n_seq, max_pages, T, dev)
     else:
-        for t, shape, n in zip(out, ((n_seq + 1,), (n_seq,), (T,), (T,), (T, max_pages), (T,),
-                                     (T,)), Batch._fields):
-            _req_on(t, torch.int64 if n == "slot_mapping" else torch.int32, shape,
-                    seq_page_table.device, n)
+        _req_on(out[0], i32, (n_seq + 1,), dev, "q_start")
+        _req_on(out[1], i32, (n_seq,), dev, "seq_len (out)")
+        _req_on(out[2], i32, (T,), dev, "tok_seq")
+        _req_on(out[3], i32, (T,), dev, "tok_pos")
+        _req_on(out[4], i32, (T, max_pages), dev, "tok_page_table")
+        _req_on(out[5], i32, (T,), dev, "tok_kv_len")
+        _req_on(out[6], torch.int64, (T,), dev, "slot_mapping")
     if err is not None:
-        _req_on(err, torch.int32, (err.numel(),), seq_page_table.device, "err")
-    with _on(seq_page_table):
-        _check(_lib.paged_batch_build(
-            seq_page_table.data_ptr(), n_seq, max_pages, seq_len.data_ptr(), new_len.data_ptr(),
-            page_ref.data_ptr(), page_ref.numel(), P, T, *[t.data_ptr() for t in out],
-            None if err is None else err.data_ptr(), _stream(stream)), "paged_batch_build")
+        _req_on(err, torch.int32, (err.numel(),), dev, "err")
+    q_start, seq_len_out, tok_seq, tok_pos, tok_page_table, tok_kv_len, slot_mapping = out
+    _call("paged_batch_build", _lib.paged_batch_build, dev,
+          (seq_page_table.data_ptr(), n_seq, max_pages, seq_len.data_ptr(), new_len.data_ptr(),
+           page_ref.data_ptr(), num_pages, P, T, q_start.data_ptr(), seq_len_out.data_ptr(),
+           tok_seq.data_ptr(), tok_pos.data_ptr(), tok_page_table.data_ptr(),
+           tok_kv_len.data_ptr(), slot_mapping.data_ptr(), None if err is None else err.data_ptr(),
+           _raw_stream(stream, dev)))
     return out
 
 
@@ -480,10 +494,9 @@ def _plan(fn_name, tok_page_table, tok_kv_len, Hq, Hkv, P, d, window, workspace,
     _req_on(tok_page_table, torch.int32, (T, max_pages), dev, "tok_page_table")
     _req_on(tok_kv_len, torch.int32, (T,), dev, "tok_kv_len")
     _req_on(workspace, torch.uint8, (workspace.numel(),), dev, "workspace")
-    with _on(tok_page_table):
-        _check(getattr(_lib, fn_name)(tok_page_table.data_ptr(), max_pages, tok_kv_len.data_ptr(),
-                                      T, Hq, Hkv, P, d, *window, workspace.data_ptr(),
-                                      workspace.numel(), _stream(stream)), fn_name)
+    _call(fn_name, getattr(_lib, fn_name), dev,
+          (tok_page_table.data_ptr(), max_pages, tok_kv_len.data_ptr(), T, Hq, Hkv, P, d, *window,
+           workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev)))
 
 
 def plan_diff(tok_page_table, tok_kv_len, Hq, Hkv, P, d, workspace, stream=None):
@@ -521,11 +534,10 @@ def _attn_on(fn_name, q, k_pages, v_pages, tok_page_table, tok_kv_len, scale, ex
         workspace = new_ws(T, Hq, Hkv, d, dev)
     else:
         _req_on(workspace, torch.uint8, (workspace.numel(),), dev, "workspace")
-    with _on(q):
-        _check(getattr(_lib, fn_name)(
-            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), tok_page_table.data_ptr(),
-            max_pages, tok_kv_len.data_ptr(), T, Hq, Hkv, P, d, N, scale, *extra, out.data_ptr(),
-            workspace.data_ptr(), workspace.numel(), _stream(stream)), fn_name)
+    _call(fn_name, getattr(_lib, fn_name), dev,
+          (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), tok_page_table.data_ptr(),
+           max_pages, tok_kv_len.data_ptr(), T, Hq, Hkv, P, d, N, scale, *extra, out.data_ptr(),
+           workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev)))
     return out
 
 

@@ -21,6 +21,7 @@ namespace pa {
 
 constexpr int kBatchCtas = 8;       // portable cluster size
 constexpr int kBatchThreads = 1024;
+constexpr int kRounds = 64;         // at most: the pool's pieces of one warp
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
@@ -88,99 +89,164 @@ __device__ __forceinline__ int first_above(const int *v, int n, int x) {
 // Pages that hold `len` positions.
 __device__ __forceinline__ int pages_of(long long len, int P) { return (int)((len + P - 1) / P); }
 
+__device__ __forceinline__ int warp_incl(int x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// Reference counts of pages p .. p + 3 of a pool of n; past its end: in use.
+__device__ __forceinline__ int4 ref4(const int32_t *ref, int p, int n) {
+  if (p + 4 <= n) return __ldcg(reinterpret_cast<const int4 *>(ref + p));
+  return make_int4(p < n ? __ldcg(ref + p) : 1, p + 1 < n ? __ldcg(ref + p + 1) : 1,
+                   p + 2 < n ? __ldcg(ref + p + 2) : 1, 1);
+}
+
 __global__ void __launch_bounds__(kBatchThreads, 1)
 k_batch_admit(BatchArgs a) {
   extern __shared__ int dyn[];
-  int *pend = dyn;            // [n_seq] pages that requests 0..i need together (saturated)
-  int *tend = dyn + a.n_seq;  // [n_seq] tokens that they add together (saturated)
+  int *pend = dyn;               // [n_seq] pages that requests 0..i need together (saturated)
+  int *tend = pend + a.n_seq;    // [n_seq] tokens that they add together (saturated)
+  int *first = tend + a.n_seq;   // [n_seq] pages that request i has
+  int *fin = first + a.n_seq;    // [n_fin] finished requests
   __shared__ long long sh[32][2];
-  __shared__ int n_free_slice;
+  __shared__ int free_cnt[kRounds][32], free_cta[kRounds], free_base[kRounds];
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x;  // the grid is one cluster
+  constexpr int kWarps = kBatchCtas * kBatchThreads / 32;
+  const int gw = rank * (kBatchThreads / 32) + warp;
   const long long cap = (long long)a.max_pages * a.P;
 
-  // 1. page and token sums over the requests.  Every CTA does this for itself: the sums are
-  //    then in its own shared memory, and n_seq is small beside a cluster barrier's cost.
+  // 1. page and token sums over the requests, and the list of the finished ones (counted in
+  //    the token sum's upper bits: at most 2^13 requests of at most 2^30 tokens).  Every CTA
+  //    does this for itself: the sums are then in its own shared memory, and n_seq is small
+  //    beside a cluster barrier's cost.
+  constexpr int kFinBit = 48;
+  constexpr long long kTokMask = (1ll << kFinBit) - 1;
   long long need_all = 0, toks_all = 0;
-  int any_finished = 0;
   for (int i0 = 0; i0 < a.n_seq; i0 += kBatchThreads) {
     const int i = i0 + tid;
     long long need = 0, add = 0;
+    bool end = false;
     if (i < a.n_seq) {
       const long long len = a.seq_len[i], nw = a.new_len[i];
-      any_finished |= nw < 0;
+      end = nw < 0;
       if (nw > 0) {
         if (len < 0 || len + nw > cap) {
           if (rank == 0 && a.err) atomicOr(a.err, PA_ERR_SEQ_RANGE);
         } else {
-          need = pages_of(len + nw, a.P) - pages_of(len, a.P);
+          first[i] = pages_of(len, a.P);
+          need = pages_of(len + nw, a.P) - first[i];
           add = nw;
         }
       }
+      if (end) add = 1ll << kFinBit;
     }
     long long tn, tt;
     scan2(need, add, sh, &tn, &tt);
     if (i < a.n_seq) {
       pend[i] = (int)min(need_all + need, (long long)INT_MAX);
-      tend[i] = (int)min(toks_all + add, (long long)INT_MAX);
+      tend[i] = (int)min((toks_all + add) & kTokMask, (long long)INT_MAX);
+      if (end) fin[(int)((toks_all + add) >> kFinBit) - 1] = i;
     }
     need_all += tn;
     toks_all += tt;
   }
+  const int n_fin = (int)(toks_all >> kFinBit);
+  toks_all &= kTokMask;
+  __syncthreads();
 
-  // 2. finished requests: a warp per row; each entry's page loses one reference
-  if (__syncthreads_or(any_finished)) {
-    for (int i = rank * (kBatchThreads / 32) + warp; i < a.n_seq;
-         i += kBatchCtas * (kBatchThreads / 32)) {
-      if (a.new_len[i] >= 0) continue;
-      int32_t *row = a.seq_pt + (size_t)i * a.max_pages;
-      for (int c = lane; c < a.max_pages; c += 32) {
-        const int page = row[c];
-        if (page < 0) continue;
-        row[c] = -1;
-        if (page >= a.num_pages) {
-          if (a.err) atomicOr(a.err, PA_ERR_PAGE_RANGE);
-        } else if (atomicSub(&a.page_ref[page], 1) <= 0) {
-          // it was free already: no reference to give back (the order of two such
-          // releases does not matter, each restores what it took)
-          atomicAdd(&a.page_ref[page], 1);
-          if (a.err) atomicOr(a.err, PA_ERR_REFCOUNT);
-        }
+  // 2. finished requests: each entry's page loses one reference.  The cluster's warps share
+  //    the rows in pieces of 128 entries, four a lane, whose loads are in flight together,
+  //    and the decrements return nothing; a page that had no reference left shows below zero
+  //    in the next step.
+  if (n_fin > 0) {
+    const int pieces = (a.max_pages + 127) / 128;
+    for (long long u = gw; u < (long long)n_fin * pieces; u += kWarps) {
+      const int f = (int)(u / pieces), x = (int)(u - (long long)f * pieces);
+      int32_t *row = a.seq_pt + (size_t)fin[f] * a.max_pages;
+      int page[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = x * 128 + k * 32 + lane;
+        page[k] = c < a.max_pages ? row[c] : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (page[k] < 0) continue;
+        row[x * 128 + k * 32 + lane] = -1;
+        if (page[k] < a.num_pages) atomicSub(&a.page_ref[page[k]], 1);
+        else if (a.err) atomicOr(a.err, PA_ERR_PAGE_RANGE);
       }
     }
     __threadfence();
     cluster_sync();  // the counts below see every release (they read past L1)
   }
 
-  // 3. free pages.  CTA r owns a contiguous slice of the pool and a thread a contiguous
-  //    piece of the slice, so one block scan ranks every free page by id.
-  const int per_thread = (int)(((long long)a.num_pages + kBatchCtas * kBatchThreads * 4 - 1) /
-                               (kBatchCtas * kBatchThreads * 4)) * 4;
-  const long long g0 = ((long long)rank * kBatchThreads + tid) * per_thread;
-  const int p0 = (int)min(g0, (long long)a.num_pages);
-  const int p1 = (int)min(g0 + per_thread, (long long)a.num_pages);
-  int rank0 = 0;       // free pages before this thread's
+  // 3. free pages.  The pool is cut into rounds of kWarps pieces; warp gw of the cluster counts
+  //    piece gw of every round, 128 pages at a time (16 bytes a lane), and a scan over
+  //    (round, CTA) ranks every free page by id.  So the first pages, which are handed out
+  //    first, are spread over all warps (one contiguous piece per warp left the few warps that
+  //    own them a serial walk).  Counts below zero, a free page's release, become zero again.
+  const int piece = max(1, (int)(((long long)a.num_pages + kWarps * 128ll * kRounds - 1) /
+                                 (kWarps * 128ll * kRounds))) * 128;
+  const int rounds = (int)(((long long)a.num_pages + (long long)kWarps * piece - 1) /
+                           ((long long)kWarps * piece));
+  const bool count = need_all > 0 || n_fin > 0;
   long long free_all = 0;
-  if (need_all > 0) {
-    long long mine = 0, zero = 0, total, unused;
-    int p = p0;
-    for (; p + 4 <= p1; p += 4) {
-      const int4 v = __ldcg(reinterpret_cast<const int4 *>(a.page_ref + p));
-      mine += (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
+  if (count) {
+    int low = 0;
+    constexpr int kAhead = 4;  // rounds whose loads are in flight together
+    for (int r = 0; r < rounds; r += kAhead) {
+      int n[kAhead] = {};
+      // whole rounds load without a branch, or the loads would wait for one another
+      const bool full = (long long)(r + kAhead) * kWarps * piece <= a.num_pages;
+      for (int o = 4 * lane; o < piece; o += 128) {
+        int4 v[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const long long p = ((long long)(r + k) * kWarps + gw) * piece + o;
+          if (full) v[k] = __ldcg(reinterpret_cast<const int4 *>(a.page_ref + p));
+          else v[k] = p < a.num_pages ? ref4(a.page_ref, (int)p, a.num_pages)
+                                      : make_int4(1, 1, 1, 1);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          n[k] += (v[k].x <= 0) + (v[k].y <= 0) + (v[k].z <= 0) + (v[k].w <= 0);
+          low = min(low, min(min(v[k].x, v[k].y), min(v[k].z, v[k].w)));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int sum = __reduce_add_sync(0xffffffffu, n[k]);
+        if (lane == 0 && r + k < rounds) free_cnt[r + k][warp] = sum;
+      }
     }
-    for (; p < p1; ++p) mine += __ldcg(a.page_ref + p) == 0;
-    long long incl = mine;
-    scan2(incl, zero, sh, &total, &unused);
-    if (tid == 0) n_free_slice = (int)total;
+    if (__any_sync(0xffffffffu, low < 0)) {
+      if (lane == 0 && a.err) atomicOr(a.err, PA_ERR_REFCOUNT);
+      for (int r = 0; r < rounds; ++r) {
+        const long long q0 = ((long long)r * kWarps + gw) * piece;
+        for (long long p = q0 + lane; p < min(q0 + piece, (long long)a.num_pages); p += 32)
+          if (__ldcg(a.page_ref + p) < 0) a.page_ref[p] = 0;
+      }
+    }
+    __syncthreads();
+    for (int r = warp; r < rounds; r += kBatchThreads / 32) {  // this CTA's pages per round
+      const int n = __reduce_add_sync(0xffffffffu, free_cnt[r][lane]);
+      if (lane == 0) free_cta[r] = n;
+    }
     cluster_sync();
-    long long before = 0;
-    for (int r = 0; r < kBatchCtas; ++r) {
-      const int n = ld_cluster(&n_free_slice, r);
-      if (r < rank) before += n;
-      free_all += n;
-    }
-    rank0 = (int)(before + incl - mine);
+    long long n = 0, zero = 0, unused;
+    if (tid < rounds * kBatchCtas) n = ld_cluster(&free_cta[tid / kBatchCtas], tid % kBatchCtas);
+    const long long mine = n;
+    scan2(n, zero, sh, &free_all, &unused);
+    if (tid < rounds * kBatchCtas && tid % kBatchCtas == rank)
+      free_base[tid / kBatchCtas] = (int)(n - mine);  // free pages before this CTA's of the round
+    __syncthreads();
   }
 
   // 4. the longest prefix of the requests whose pages and tokens fit
@@ -192,19 +258,31 @@ k_batch_admit(BatchArgs a) {
   if (rank == 0 && tid == 0 && a.err && (n_tok < toks_all)) atomicOr(a.err, PA_ERR_NO_SPACE);
 
   // 5. the r-th free page goes to the request whose page range holds r
-  if (n_take > rank0) {
-    int r = rank0, i = -1, i_end = 0, i_beg = 0, first = 0;
-    for (int p = p0; p < p1 && r < n_take; ++p) {
-      if (__ldcg(a.page_ref + p) != 0) continue;
-      if (i < 0 || r >= i_end) {
-        i = first_above(pend, n_adm, r);
-        i_end = pend[i];
-        i_beg = i > 0 ? pend[i - 1] : 0;
-        first = pages_of(a.seq_len[i], a.P);
+  for (int rd = 0; n_take > 0 && rd < rounds; ++rd) {
+    int base = free_base[rd];
+    if (base >= n_take) break;
+    base += __reduce_add_sync(0xffffffffu, lane < warp ? free_cnt[rd][lane] : 0);
+    const long long q0 = ((long long)rd * kWarps + gw) * piece;
+    const int p1 = (int)min(q0 + piece, (long long)a.num_pages);
+    for (long long p = q0; p < p1 && base < n_take; p += 128) {
+      const int q = (int)p + 4 * lane;
+      const int4 v = q < p1 ? ref4(a.page_ref, q, a.num_pages) : make_int4(1, 1, 1, 1);
+      const int x[4] = {v.x, v.y, v.z, v.w};
+      const int cnt = (v.x <= 0) + (v.y <= 0) + (v.z <= 0) + (v.w <= 0);
+      const int incl = warp_incl(cnt, lane);
+      int r = base + incl - cnt;
+      int i = cnt > 0 && r < n_take ? first_above(pend, n_adm, r) : 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (x[k] > 0) continue;
+        if (r < n_take) {
+          if (pend[i] <= r) i = first_above(pend, n_adm, r);
+          a.seq_pt[(size_t)i * a.max_pages + first[i] + (r - (i > 0 ? pend[i - 1] : 0))] = q + k;
+          a.page_ref[q + k] = 1;
+        }
+        ++r;
       }
-      a.seq_pt[(size_t)i * a.max_pages + first + (r - i_beg)] = p;
-      a.page_ref[p] = 1;
-      ++r;
+      base += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
 
@@ -223,7 +301,7 @@ k_batch_admit(BatchArgs a) {
     a.tok_kv[t] = s < 0 ? 0 : pos + 1;
   }
   // a CTA's shared memory stays until its neighbours have read its free-page count
-  if (need_all > 0) cluster_sync();
+  if (count) cluster_sync();
 }
 
 // Every token's table row and slot.  A warp takes kTok consecutive tokens: tokens of one
@@ -293,11 +371,11 @@ static cudaError_t launch_rows(const BatchArgs &a, int num_sms, cudaStream_t s) 
 }
 
 cudaError_t launch_batch(const BatchArgs &a, int num_sms, cudaStream_t s) {
-  const size_t smem = (size_t)a.n_seq * 8;
+  const size_t smem = (size_t)a.n_seq * 16;
   static PerDeviceOnce setup;
   if (setup.first()) {
     cudaError_t e = cudaFuncSetAttribute(k_batch_admit, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kBatchMaxSeq * 8);
+                                         kBatchMaxSeq * 16);
     if (e != cudaSuccess) return e;
     setup.mark();
   }

@@ -82,7 +82,7 @@ struct AttnArgs {
 constexpr int kDiffMaps = 2;
 
 // Arguments of the batch build (passed by value); see paged_batch_build.
-constexpr int kBatchMaxSeq = 16384;  // two sums per request in one CTA's shared memory
+constexpr int kBatchMaxSeq = 8192;  // four words per request in one CTA's shared memory
 struct BatchArgs {
   int32_t *seq_pt;
   const int32_t *seq_len, *new_len;
