@@ -353,7 +353,7 @@ static int plan_with(const int32_t *tok_page_table, int max_pages, const int32_t
   k_plan_mark<<<blocks, 256, 0, s>>>(tok_page_table, max_pages, T, ws, lay);
   if (cudaGetLastError() != cudaSuccess) return PA_ELAUNCH;
   k_plan<<<1, 1024, 0, s>>>(tok_page_table, max_pages, tok_kv_len, T, P, Hkv, NP, min_run, window,
-                            windowed, C, ws, lay);
+                            windowed, windowed || maps > 1, C, ws, lay);
   return launch_status(cudaGetLastError());
 }
 

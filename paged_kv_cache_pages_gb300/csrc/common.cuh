@@ -42,7 +42,7 @@ struct WsHeader {
   int n_dec;      // decode tokens
   int n_units;    // decode work units (token, kv head, 128-key block)
   int pf_work;    // prefill work units (item, 128-key block)
-  int C;          // CTAs the plan was cut for (= SM count)
+  int C;          // CTAs the prefill work was cut for (the SM count; see kPfMinRange)
   int T;
   int kind;       // what the plan was made for (plan_kind): a run of another kind refuses it
   int Hkv;
@@ -68,6 +68,12 @@ constexpr int kPfMinItemUnits = 6;
 __host__ __device__ inline int pf_item_units(int nkb) {
   return nkb > 0 ? (nkb > kPfMinItemUnits ? nkb : kPfMinItemUnits) : 0;
 }
+
+// Plans of the differential and the windowed attention cut their prefill work differently:
+// an item of up to kPfMinItemUnits blocks is never split (its parts would cost more to join
+// than it takes), and a CTA gets at least kPfMinRange units, so a small ubatch goes to fewer
+// CTAs instead of to parts of a block each.
+constexpr int kPfMinRange = 4;
 
 struct WsLayout {
   size_t tiles, dec_tok, tok_unit_off, flags, runs, tile_off, dec_start, pf_start, pf_cnt;

@@ -55,13 +55,18 @@ constexpr int kWarpMma = 9;
 constexpr int kBoxBytes = 128 * 128;  // 128 rows x 64 halves
 constexpr float kRescaleThreshold = 8.0f;
 
-template <int D, bool KV8 = false>
+template <int D, bool KV8 = false, bool DIFF = false>
 struct PfCfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kHalves * kBoxBytes;  // 128 rows x D halves
+  // The Q tiles of an item (one when its two maps share it), in two buffers where they fit:
+  // the next item's tiles then land while the current one runs, instead of after its last MMA
+  static constexpr int kQTiles = DIFF ? 1 : 2;
+  static constexpr int kQBufs = D == 64 || DIFF ? 2 : 1;
+  static constexpr int kQBytes = kQTiles * kTile;
   static constexpr int kQ0 = 0;
-  static constexpr int kQ1 = kTile;
-  static constexpr int kK = 2 * kTile;
+  static constexpr int kQ1 = DIFF ? 0 : kTile;
+  static constexpr int kK = kQBufs * kQBytes;
   static constexpr int kV = kK + kPfStages * kTile;
   // FP8 pages: the codes of the next K block and of the next V block wait here
   static constexpr int kStgK = kV + kPfStages * kTile;
@@ -79,7 +84,7 @@ struct PfCfg {
 };
 
 struct PfBars {
-  uint64_t q_full, q_empty;
+  uint64_t q_full[2], q_empty[2];  // per buffer
   uint64_t k_full[kPfStages], k_empty[kPfStages], v_full[kPfStages], v_empty[kPfStages];
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint64_t turn[2];  // issuer turns: tile 1's issuer -> tile 0's, tile 0's -> tile 1's
@@ -231,6 +236,13 @@ struct SegCtx {
   int item_heads;  // query heads of an item: a pair, or one (DIFF: its two maps are the pair)
 };
 
+__device__ __forceinline__ void seg_heads(Seg &s, const SegCtx &x) {
+  s.g = s.j / x.NP;
+  const int pair = s.j - s.g * x.NP;
+  s.h0 = x.G >= 2 ? s.g * x.G + x.item_heads * pair : s.g;
+  s.h1 = s.h0 + 1;
+}
+
 __device__ __forceinline__ void seg_load(Seg &s, const SegCtx &x) {
   int4 tl = x.tiles[s.tile];
   s.tile_start = tl.x;
@@ -238,10 +250,7 @@ __device__ __forceinline__ void seg_load(Seg &s, const SegCtx &x) {
   s.lo_off = tl.y >> 16;
   s.nkb = tl.z;
   s.max_kv = tl.w;
-  s.g = s.j / x.NP;
-  const int pair = s.j - s.g * x.NP;
-  s.h0 = x.G >= 2 ? s.g * x.G + x.item_heads * pair : s.g;
-  s.h1 = s.h0 + 1;
+  seg_heads(s, x);
   s.kb0 = (s.max_kv + KB - 1) / KB - s.nkb;
   // an item spans pf_item_units(nkb) units: its key blocks, then virtual ones (no work)
   s.item_start = (long long)x.tile_off[s.tile] + (long long)s.j * pf_item_units(s.nkb);
@@ -250,10 +259,13 @@ __device__ __forceinline__ void seg_load(Seg &s, const SegCtx &x) {
 // The next item, in the next tile that has keys when this tile's items are done (there
 // is one: the caller checked that units are left before the end of the run).
 __device__ __forceinline__ void seg_next_item(Seg &s, const SegCtx &x) {
-  if (++s.j == x.items_per_tile) {
-    s.j = 0;
-    do { ++s.tile; } while (x.tiles[s.tile].z == 0);
+  if (++s.j < x.items_per_tile) {  // the same tile: nothing to load
+    s.item_start += pf_item_units(s.nkb);
+    seg_heads(s, x);
+    return;
   }
+  s.j = 0;
+  do { ++s.tile; } while (x.tiles[s.tile].z == 0);
   seg_load(s, x);
 }
 
@@ -311,9 +323,12 @@ struct PfWork {
   SegCtx sx;
   int4 start;           // first (tile, item, key block) of this CTA
   long long W, w0, w1;  // total work units; this CTA's range [w0, w1)
+  long long cut0;       // where an even cut would start the range (w0 may lie before it)
   int C;                // CTAs the plan was cut for
 };
 
+// WHOLE: a plan that keeps short items whole (differential and windowed attention).
+template <bool WHOLE = false>
 __device__ __forceinline__ PfWork pf_work(const AttnArgs &a, int NP, int G, int item_heads = 2) {
   uint64_t wsp = reinterpret_cast<uint64_t>(a.ws);
   asm volatile("" : "+l"(wsp));
@@ -323,7 +338,7 @@ __device__ __forceinline__ PfWork pf_work(const AttnArgs &a, int NP, int G, int 
   r.C = hdr->C;
   r.W = hdr->pf_work;
   const int c = blockIdx.x;
-  r.w0 = (long long)c * r.W / r.C;
+  r.cut0 = r.w0 = (long long)c * r.W / r.C;
   r.w1 = (long long)(c + 1) * r.W / r.C;
   r.sx.tiles = reinterpret_cast<const int4 *>(ws + a.lay.tiles);
   r.sx.tile_off = reinterpret_cast<const int *>(ws + a.lay.tile_off);
@@ -333,6 +348,17 @@ __device__ __forceinline__ PfWork pf_work(const AttnArgs &a, int NP, int G, int 
   r.sx.item_heads = item_heads;
   r.sx.items_per_tile = a.Hkv * NP;
   r.start = reinterpret_cast<const int4 *>(ws + a.lay.pf_start)[c];
+  if (WHOLE) {
+    // the planner moved cuts in short items back to the items' starts
+    auto unit_of = [&](int4 p) {
+      return (long long)r.sx.tile_off[p.x] + (long long)p.y * pf_item_units(r.sx.tiles[p.x].z) +
+             p.z;
+    };
+    r.w0 = r.W > 0 ? unit_of(r.start) : 0;
+    r.w1 = c + 1 == r.C || r.W == 0
+               ? r.W
+               : unit_of(reinterpret_cast<const int4 *>(ws + a.lay.pf_start)[c + 1]);
+  }
   return r;
 }
 
@@ -409,11 +435,11 @@ __device__ __forceinline__ void kv8_widen_role(const AttnArgs &a, const AttnMaps
                    : make_float4(0.f, 0.f, 0.f, 0.f);
   };
   auto load_q = [&](int ts, int h0, int h1) {
-    mbar_arrive_expect_tx(&bars->q_full, NQ * Cfg::kTile);
+    mbar_arrive_expect_tx(&bars->q_full[0], NQ * Cfg::kTile);
     for (int hf = 0; hf < Cfg::kHalves; ++hf) {
-      tc::tma_load_3d(smem + Cfg::kQ0 + hf * kBoxBytes, &maps.q, hf * 64, h0, ts, &bars->q_full);
+      tc::tma_load_3d(smem + Cfg::kQ0 + hf * kBoxBytes, &maps.q, hf * 64, h0, ts, &bars->q_full[0]);
       if (NQ == 2)
-        tc::tma_load_3d(smem + Cfg::kQ1 + hf * kBoxBytes, &maps.q, hf * 64, h1, ts, &bars->q_full);
+        tc::tma_load_3d(smem + Cfg::kQ1 + hf * kBoxBytes, &maps.q, hf * 64, h1, ts, &bars->q_full[0]);
     }
   };
   if (!more) return;
@@ -491,7 +517,7 @@ __device__ __forceinline__ void kv8_widen_role(const AttnArgs &a, const AttnMaps
     if (ISK && first) {
       // a new item: its Q tiles once the previous item's MMAs have released them
       if (nitem > 0) {
-        if (!__all_sync(~0u, lane != 0 || pf_wait(&bars->q_empty, (nitem - 1) & 1, err, abort)))
+        if (!__all_sync(~0u, lane != 0 || pf_wait(&bars->q_empty[0], (nitem - 1) & 1, err, abort)))
           break;
         if (lane == 0) load_q(ts, h0, h1);
       }
@@ -531,9 +557,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   constexpr bool MASK = VAR == kPfMask, KV8 = VAR == kPfKv8;
   constexpr bool DIFF = VAR == kPfDiff, WIN = VAR == kPfWin;
+  constexpr bool JOIN = DIFF || WIN;  // split items are joined by k_prefill_join
   constexpr int kItemHeads = DIFF ? 1 : 2;
   static_assert(!KV8 || D == 128, "FP8 pages: d 128");
-  using Cfg = PfCfg<D, KV8>;
+  using Cfg = PfCfg<D, KV8, DIFF>;
   // rows of a split part's record: O[D] | m | l | 2 unused (D + 4 rows of 128 floats)
   constexpr int kPartStride = D + 4;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -550,6 +577,9 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = hdr->C;
   const int c = blockIdx.x;
+  // the join behind this kernel may take the SMs that this grid's CTAs leave (it waits for the
+  // whole grid before it reads anything)
+  if (JOIN) asm volatile("griddepcontrol.launch_dependents;");
   if (c >= C) return;
   if (hdr->kind != plan_kind(NP, WIN)) {  // the tile records are another operator's
     if (c == 0 && tid == 0) atomicOr(err, PA_ERR_PLAN);
@@ -564,13 +594,15 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       reinterpret_cast<uint4 *>(a.out + (size_t)tl.x * a.Hq * D)[x] = make_uint4(0, 0, 0, 0);
   }
   {
-    const PfWork pw = pf_work(a, NP, G, kItemHeads);
+    const PfWork pw = pf_work<JOIN>(a, NP, G, kItemHeads);
     if (pw.w0 >= pw.w1) return;
   }
   if (tid == 0) {
     // stages and Q tiles are released by both MMA-issuing threads (one per query tile)
-    mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, NQ);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars->q_full[b], 1);
+      mbar_init(&bars->q_empty[b], NQ);
+    }
     for (int s = 0; s < kPfStages; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->k_empty[s], NQ);
@@ -615,10 +647,13 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
     kv8_widen_role<true>(a, maps, bars, smem, err, abort, lane, NQ, NP, G);
    } else if (KV8 && warp == kWarpTma + 3) {
     kv8_widen_role<false>(a, maps, bars, smem, err, abort, lane, NQ, NP, G);
-   } else if (!KV8 && warp == kWarpTma && lane == 0) {
+   } else if (!KV8 && warp == kWarpTma) {
     // ------------------------------------------------------------ TMA producer
+    // The whole warp: a lane issues one box (page j, 64-column half) of a block, so the page
+    // ids of a block of small pages are looked up and its boxes issued side by side (one
+    // thread after the other halved the rate at page size 16).  Lane 0 waits for the warp.
     {
-      const PfWork pw = pf_work(a, NP, G, kItemHeads);
+      const PfWork pw = pf_work<JOIN>(a, NP, G, kItemHeads);
       const SegCtx &sx = pw.sx;
       uint32_t it = 0;
       int nitem = 0;
@@ -626,15 +661,11 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       const int oob_row = a.num_pages * a.Hkv * a.P;  // first row past the pool: zero fill
       Seg w{};
       const int32_t *row = nullptr;
-      // row coordinate of page j of key block kb in the pool map (past the end when
-      // invalid: the box is zero-filled and nothing outside the pool is touched)
-      auto ycoord = [&](int kb, int j) {
-        int page = row[((WIN ? w.kb0 : 0) + kb) * pages_per_block + j];
-        if (page < 0 || page >= a.num_pages) {
-          atomicOr(err, PA_ERR_PAGE_RANGE);
-          return oob_row;
-        }
-        return (page * a.Hkv + w.g) * a.P;
+      const int box_j = lane / Cfg::kHalves, box_hf = lane % Cfg::kHalves;
+      auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
+        int ok = 0;
+        if (lane == 0) ok = pf_wait(bar, parity, err, abort) ? 1 : 0;
+        return __shfl_sync(0xffffffffu, ok, 0) != 0;
       };
       // K and V boxes of key block kb into ring stage it % kPfStages
       auto load_kv = [&](int kb) -> bool {
@@ -645,41 +676,51 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         // windowed: pages before the tile's first visible key are not looked at
         const int j0 = WIN && kb == 0 ? w.lo_off / a.P : 0;
         const uint32_t bytes = (uint32_t)(npg - j0) * a.P * 128u * Cfg::kHalves;
-        if (!pf_wait(&bars->k_empty[st], ph ^ 1u, err, abort)) return false;
-        mbar_arrive_expect_tx(&bars->k_full[st], bytes);
-        for (int j = j0; j < npg; ++j)
-          for (int hf = 0; hf < Cfg::kHalves; ++hf)
-            tc::tma_load_2d(smem + Cfg::kK + st * Cfg::kTile + hf * kBoxBytes + j * a.P * 128,
-                            &maps.k, hf * 64, ycoord(kb, j), &bars->k_full[st]);
-        if (!pf_wait(&bars->v_empty[st], ph ^ 1u, err, abort)) return false;
-        mbar_arrive_expect_tx(&bars->v_full[st], bytes);
-        for (int j = j0; j < npg; ++j)
-          for (int hf = 0; hf < Cfg::kHalves; ++hf)
-            tc::tma_load_2d(smem + Cfg::kV + st * Cfg::kTile + hf * kBoxBytes + j * a.P * 128,
-                            &maps.v, hf * 64, ycoord(kb, j), &bars->v_full[st]);
+        // this lane's box: its row coordinate in the pool map (past the end when the page is
+        // invalid: the box is zero-filled and nothing outside the pool is touched)
+        const bool mine = box_j >= j0 && box_j < npg;
+        int y = oob_row;
+        if (mine) {
+          const int page = row[((WIN ? w.kb0 : 0) + kb) * pages_per_block + box_j];
+          if (page < 0 || page >= a.num_pages) atomicOr(err, PA_ERR_PAGE_RANGE);
+          else y = (page * a.Hkv + w.g) * a.P;
+        }
+        const uint32_t off = st * Cfg::kTile + box_hf * kBoxBytes + box_j * a.P * 128;
+        if (!wait_all(&bars->k_empty[st], ph ^ 1u)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], bytes);
+        __syncwarp();
+        if (mine) tc::tma_load_2d(smem + Cfg::kK + off, &maps.k, box_hf * 64, y, &bars->k_full[st]);
+        if (!wait_all(&bars->v_empty[st], ph ^ 1u)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(&bars->v_full[st], bytes);
+        __syncwarp();
+        if (mine) tc::tma_load_2d(smem + Cfg::kV + off, &maps.v, box_hf * 64, y, &bars->v_full[st]);
         ++it;
         return true;
       };
       for (bool more = seg_first(w, sx, pw); more; more = seg_next(w, sx)) {
         row = a.tpt + (size_t)w.tile_start * a.max_pages;
         int kb = w.kb_b;
-        if (nitem > 0) {
-          // the first key block of this item goes into the ring before the Q tiles wait for
-          // the previous item to release them
-          if (!load_kv(kb++)) break;
-          if (!pf_wait(&bars->q_empty, (nitem - 1) & 1, err, abort)) break;
+        const int qb = nitem % Cfg::kQBufs;
+        if (nitem >= Cfg::kQBufs) {
+          // one buffer: the first key block of this item goes into the ring before the Q tiles
+          // wait for the previous item to release them
+          if (Cfg::kQBufs == 1 && !load_kv(kb++)) break;
+          if (!wait_all(&bars->q_empty[qb], (nitem / Cfg::kQBufs - 1) & 1)) break;
         }
-        mbar_arrive_expect_tx(&bars->q_full, (DIFF ? 1 : NQ) * Cfg::kTile);
-        for (int hf = 0; hf < Cfg::kHalves; ++hf) {
-          tc::tma_load_3d(smem + Cfg::kQ0 + hf * kBoxBytes, &maps.q, hf * 64, w.h0, w.tile_start,
-                          &bars->q_full);
-          if (!DIFF && NQ == 2)
-            tc::tma_load_3d(smem + Cfg::kQ1 + hf * kBoxBytes, &maps.q, hf * 64, w.h1,
-                            w.tile_start, &bars->q_full);
+        if (lane == 0) {
+          unsigned char *q = smem + qb * Cfg::kQBytes;
+          mbar_arrive_expect_tx(&bars->q_full[qb], (DIFF ? 1 : NQ) * Cfg::kTile);
+          for (int hf = 0; hf < Cfg::kHalves; ++hf) {
+            tc::tma_load_3d(q + Cfg::kQ0 + hf * kBoxBytes, &maps.q, hf * 64, w.h0, w.tile_start,
+                            &bars->q_full[qb]);
+            if (!DIFF && NQ == 2)
+              tc::tma_load_3d(q + Cfg::kQ1 + hf * kBoxBytes, &maps.q, hf * 64, w.h1,
+                              w.tile_start, &bars->q_full[qb]);
+          }
         }
-        {  // the next item's Q tiles into L2, so that its load at the switch is short
+        if (Cfg::kQBufs == 1) {  // the next item's Q tiles into L2, so that its load at the switch is short
           Seg nx = w;
-          if (seg_next(nx, sx))
+          if (seg_next(nx, sx) && lane == 0)
             for (int hf = 0; hf < Cfg::kHalves; ++hf) {
               tc::tma_prefetch_3d(&maps.q, hf * 64, nx.h0, nx.tile_start);
               if (!DIFF && NQ == 2)
@@ -698,7 +739,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
     // One thread per query tile: warp 9 issues tile 0's MMAs, warp 10 tile 1's.  Each
     // thread's waits then leave the tensor pipe to the other thread's MMAs.
     const int qi = warp - kWarpMma;
-    const PfWork pw = pf_work(a, NP, G, kItemHeads);
+    const PfWork pw = pf_work<JOIN>(a, NP, G, kItemHeads);
     const SegCtx &sx = pw.sx;
     constexpr uint32_t idS = tc::idesc_f16(128, 128, false);
     // V: MN-major ([key][d] rows) for binary16 pages; K-major ([d][key] rows) for FP8
@@ -716,19 +757,21 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
     const uint32_t lK0 = tc::sdesc_lo(sK, 16), lK1 = tc::sdesc_lo(sK + Cfg::kTile, 16);
     const uint32_t lV0 = tc::sdesc_lo(sV, KV8 ? 16 : kBoxBytes),
                    lV1 = tc::sdesc_lo(sV + Cfg::kTile, KV8 ? 16 : kBoxBytes);
-    auto issue_S = [&](int i, int st) {
+    // (Q buffer qb)
+    auto issue_S = [&](int i, int st, int qb) {
       const uint32_t d = tmem + i * 128;
+      const uint32_t q16 = Cfg::kQBufs == 1 ? 0u : (uint32_t)(qb * Cfg::kQBytes) >> 4;
       if constexpr (DIFF) {
         // map i: the i-th half of the Q and K rows (a 64-column box at d = 128, 64 bytes of
         // the rows at d = 64: a k-step of 32 bytes never crosses a box)
         const uint32_t m16 = i ? (D == 128 ? kBoxBytes : 64) >> 4 : 0u;
-        const uint32_t a0 = tc::opaque(lQ0 + m16), b0 = tc::opaque((st ? lK1 : lK0) + m16);
+        const uint32_t a0 = tc::opaque(lQ0 + q16 + m16), b0 = tc::opaque((st ? lK1 : lK0) + m16);
         tc::mma_ss_lo<0>(d, a0, b0, idS);
 #pragma unroll
         for (int kk = 1; kk < D / 32; ++kk) tc::mma_ss_lo<1>(d, a0 + 2 * kk, b0 + 2 * kk, idS);
         return;
       }
-      const uint32_t a0 = tc::opaque(i ? lQ1 : lQ0), b0 = tc::opaque(st ? lK1 : lK0);
+      const uint32_t a0 = tc::opaque((i ? lQ1 : lQ0) + q16), b0 = tc::opaque(st ? lK1 : lK0);
       tc::mma_ss_lo<0>(d, a0, b0, idS);
 #pragma unroll
       for (int kk = 1; kk < D / 16; ++kk) {
@@ -762,12 +805,13 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
     Seg w;
     for (bool more = seg_first(w, sx, pw); more; more = seg_next(w, sx)) {
       const int nseg = w.kb_e - w.kb_b;
-      bool ok = pf_wait(&bars->q_full, nitem & 1, err, abort);
+      const int qb = nitem % Cfg::kQBufs;
+      bool ok = pf_wait(&bars->q_full[qb], (nitem / Cfg::kQBufs) & 1, err, abort);
       const int st0 = it % kPfStages;
       ok = ok && pf_wait(&bars->k_full[st0], (it / kPfStages) & 1u, err, abort);
       if (!ok) break;
       tc::fence_after_sync();
-      issue_S(qi, st0);
+      issue_S(qi, st0, qb);
       tc::commit(&bars->s_full[qi]);
       tc::commit(&bars->k_empty[st0]);
       for (int kk = 0; kk < nseg; ++kk) {
@@ -836,14 +880,14 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         if (last) tc::commit(&bars->o_full[qi]);
         tc::commit(&bars->v_empty[st]);
         if (!last) {
-          issue_S(qi, st2);
+          issue_S(qi, st2, qb);
           tc::commit(&bars->s_full[qi]);
           tc::commit(&bars->k_empty[st2]);
         }
         if (NQ == 2) mbar_arrive(&bars->turn[qi ^ 1]);
       }
       if (!ok) break;
-      tc::commit(&bars->q_empty);
+      tc::commit(&bars->q_empty[qb]);
       it += nseg;
       sc += nseg;
       ++nitem;
@@ -859,20 +903,22 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
     const uint32_t tS = tmem + wg * 128 + lane_off;
     const uint32_t tO = tmem + 256 + wg * D + lane_off;
     if (wg < NQ) {
-      const PfWork pw = pf_work(a, NP, G, kItemHeads);
+      const PfWork pw = pf_work<JOIN>(a, NP, G, kItemHeads);
       const SegCtx &sx = pw.sx;
-      const long long W = pw.W, w0 = pw.w0;
+      const long long W = pw.W, cut0 = pw.cut0;
       const int C = pw.C;
       uint32_t sc = 0;
       int nitem = 0, nwhole = 0;
       float *parts = reinterpret_cast<float *>(a.ws + a.lay.partials);
       int *cnt = reinterpret_cast<int *>(a.ws + a.lay.pf_cnt);
       Seg w;
+      int l_tile = -1, L = 0;  // the row's kv_len, loaded once per tile
       for (bool more = seg_first(w, sx, pw); more; more = seg_next(w, sx)) {
         const int h = !DIFF && wg ? w.h1 : w.h0;
         const int tok = w.tile_start + row;
         const bool valid = row < w.n_tok;
-        const int L = valid ? min(max(a.kv[tok], 0), cap) : 0;
+        if (w.tile != l_tile) L = valid ? min(max(a.kv[tok], 0), cap) : 0;
+        l_tile = w.tile;
         const int lo = WIN ? max(L - window, 0) : 0;  // first visible key
         // masked variant: this row's (sequence, position); -2 matches no cell
         const int my_seq = MASK && valid ? a.tok_seq[tok] : -2;
@@ -894,7 +940,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         const bool split = w.kb_b != 0 || w.kb_e != w.nkb;
         for (int kk = 0; kk < nseg; ++kk) {
           const int kb = w.kb_b + kk;
-          if (split && kk + 1 == nseg && wl == 0 && lane == 0) {
+          if (!JOIN && split && kk + 1 == nseg && wl == 0 && lane == 0) {
             // the records of the item's other parts, which this warpgroup may combine
             // after this block: into L2 now (one written long ago may have left it)
             const long long ie = w.item_start + w.nkb;
@@ -950,8 +996,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
               t[j] = (mw[j >> 5] >> (j & 31)) & 1u ? t[j] : 0xff800000u;
           } else if (!wfull) {
 #pragma unroll
-            for (int j = 0; j < 128; ++j)
-              t[j] = j < nv && (!WIN || j >= nlo) ? t[j] : 0xff800000u;  // -inf
+            for (int j = 0; j < 128; ++j) t[j] = j < nv && (!WIN || j >= nlo) ? t[j] : 0xff800000u;  // -inf
           }
           float mx = -INFINITY;
 #pragma unroll
@@ -1132,7 +1177,8 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           // one part of a split item: leave (O unnormalised, m, l) in this CTA's slot.  A
           // slot holds D + 2 rows of 128 floats (element-major: element e of query row r
           // at [e][r]), so that a warp's accesses to one element are one 128-byte line.
-          const bool first_seg = w.item_start <= w0;
+          // (an item that is split has the cuts of an even division inside it)
+          const bool first_seg = w.item_start <= cut0;
           const int my_slot = 2 * c + (first_seg ? 0 : 1);
           auto slot_base = [&](int sl) {
             return parts + ((size_t)sl * 2 + wg) * (size_t)kPartStride * 128 + row;
@@ -1150,6 +1196,11 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           tc::fence_before_sync();
           mbar_arrive(&bars->o_empty[wg]);
           if (DIFF) mbar_arrive(&bars->o_empty[wg ^ 1]);  // this warpgroup does not read it
+          if (JOIN) {  // k_prefill_join folds the parts
+            sc += nseg;
+            ++nitem;
+            continue;
+          }
           // count the parts that have landed; the last one combines (no waiting)
           const long long item_end = w.item_start + w.nkb;
           const int c1 = cta_of_unit(w.item_start, W, C), c2 = cta_of_unit(item_end - 1, W, C);
@@ -1157,69 +1208,13 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           for (int cc = c1; cc <= c2; ++cc) n_parts += cta_has_units(cc, W, C) ? 1 : 0;
           // one counter per (item, warpgroup, warp): a warp's 32 rows only need the same
           // 32 rows of the other parts, so warps decide independently (no cross-warp wait)
-          // (DIFF: one per (item, warp), counting both maps' parts)
-          int *my_cnt =
-              &cnt[((w.tile * sx.items_per_tile + w.j) * 2 + (DIFF ? 0 : wg)) * 4 + wl];
+          int *my_cnt = &cnt[((w.tile * sx.items_per_tile + w.j) * 2 + wg) * 4 + wl];
           __threadfence();
           __syncwarp();
           int old = 0;
           if (lane == 0) old = atomicAdd(my_cnt, 1);
           old = __shfl_sync(0xffffffffu, old, 0);
-          if (DIFF && old == 2 * n_parts - 1) {
-            // Both maps of all parts have landed: y = sum over parts of c0 O_0 - c1 O_1 with
-            // c_i = 2^(m_i - M_i) / L_i (lam in c1), one record chunk after the other.
-            __threadfence();
-            auto rec_of = [&](int cc, int map) {
-              const int sl = 2 * cc + (w.item_start <= (long long)cc * W / C ? 0 : 1);
-              return parts + ((size_t)sl * 2 + map) * (size_t)kPartStride * 128 + row;
-            };
-            float M[2] = {-INFINITY, -INFINITY}, Ls[2] = {0.f, 0.f};
-            for (int cc = c1; cc <= c2; ++cc) {
-              if (!cta_has_units(cc, W, C)) continue;
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float *r = rec_of(cc, i);
-                const float mp = __ldcg(r + D * 128), lp = __ldcg(r + (D + 1) * 128);
-                const float Mn = fmaxf(M[i], mp);
-                const float fo = M[i] == -INFINITY ? 0.f : exp2_approx(M[i] - Mn);
-                const float fp = mp == -INFINITY ? 0.f : exp2_approx(mp - Mn);
-                Ls[i] = __fmaf_rn(lp, fp, __fmul_rn(Ls[i], fo));
-                M[i] = Mn;
-              }
-            }
-            const float i0 = Ls[0] > 0.f ? 1.f / Ls[0] : 0.f;
-            const float i1 = Ls[1] > 0.f ? -__ldg(a.lam + h) / Ls[1] : 0.f;
-            float y[D];
-#pragma unroll
-            for (int e = 0; e < D; ++e) y[e] = 0.f;
-            for (int cc = c1; cc <= c2; ++cc) {
-              if (!cta_has_units(cc, W, C)) continue;
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float *r = rec_of(cc, i);
-                const float mp = __ldcg(r + D * 128);
-                const float cf = mp == -INFINITY ? 0.f : exp2_approx(mp - M[i]) * (i ? i1 : i0);
-#pragma unroll
-                for (int e = 0; e < D; ++e) y[e] = __fmaf_rn(__ldcg(r + e * 128), cf, y[e]);
-              }
-            }
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < D; ++e) ss = __fmaf_rn(y[e], y[e], ss);
-            const float f = diff_scale(ss);
-            if (valid) {
-#pragma unroll
-              for (int q = 0; q < D / 8; ++q) {
-                uint32_t hw[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  hw[e] = diff_pack(y[q * 8 + 2 * e], y[q * 8 + 2 * e + 1], q * 8 + 2 * e, f);
-                orow[q] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-              }
-            }
-            if (lane == 0) *my_cnt = 0;  // ready for the next run of this plan
-          }
-          if (!DIFF && old == n_parts - 1) {
+          if (old == n_parts - 1) {
             __threadfence();
             // Parts are folded in CTA order with the same arithmetic whichever CTA
             // combines, so results are reproducible.  The other parts were written by
@@ -1266,7 +1261,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
                 fk[k] = (mk[k] == -INFINITY) ? 0.f : exp2_approx(mk[k] - M);
                 if (k < np) Ls += (mk[k] == -INFINITY) ? 0.f : lk[k] * fk[k];
               }
-              const float inv = row_inv(M, Ls);
+              const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
               float vb[2][kFastParts][16];
               auto load_chunk = [&](int ch, float (&v)[kFastParts][16]) {
 #pragma unroll
@@ -1306,7 +1301,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
                 const float l_p = cc == c ? l_run : __ldcg(r + (D + 1) * 128);
                 Ls += (m_p == -INFINITY) ? 0.f : l_p * exp2_approx(m_p - M);
               }
-              const float inv = row_inv(M, Ls);
+              const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
 #pragma unroll
               for (int ch = 0; ch < D / 16; ++ch) {
                 float acc[16];
@@ -1355,10 +1350,127 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   }
 }
 
+// The parts of the split items of a differential (DIFF) or windowed plan, folded into the
+// output.  The item cut by CTA c's first unit, if CTA c - 1 holds its first key block, is CTA
+// c's to join, 32 of its rows to each CTA of the column; a thread has one row (a warp's reads of
+// one element of 32 rows are one line) and D / 8 of its values.  As a launch of its own, any
+// number of parts is read at the rate of the whole GPU: the last part's softmax warps took 70 us
+// for ten parts (an L2 round trip at a time), and their code cost the whole blocks registers.
+template <int D, bool DIFF>
+__global__ void __launch_bounds__(256) k_prefill_join(AttnArgs a) {
+  constexpr int NM = DIFF ? 2 : 1, E = D / 8, kStride = D + 4;
+  __shared__ float sq[8][32];
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const WsHeader *hdr = reinterpret_cast<const WsHeader *>(a.ws);
+  const int G = a.Hq / a.Hkv, NP = DIFF ? G : G >= 2 ? G / 2 : 1;
+  const int C = hdr->C, c = blockIdx.x + 1;
+  const long long W = hdr->pf_work;
+  if (hdr->kind != plan_kind(NP, !DIFF) || c >= C || W <= 0) return;
+  const int4 st = reinterpret_cast<const int4 *>(a.ws + a.lay.pf_start)[c];  // tile, item, block
+  if (st.z == 0) return;  // the range starts at an item's start
+  const int4 tl = reinterpret_cast<const int4 *>(a.ws + a.lay.tiles)[st.x];
+  const long long u0 = (long long)reinterpret_cast<const int *>(a.ws + a.lay.tile_off)[st.x] +
+                       (long long)st.y * pf_item_units(tl.z);
+  const int c1 = cta_of_unit(u0, W, C), c2 = cta_of_unit(u0 + tl.z - 1, W, C);
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int n_tok = tl.y & 0xffff, row = blockIdx.y * 32 + lane;
+  if (c1 != c - 1 || blockIdx.y * 32 >= n_tok) return;
+  const int g = st.y / NP, x = st.y - g * NP;
+  const bool valid = row < n_tok;
+  const size_t tok = (size_t)(tl.x + min(row, n_tok - 1));
+  const float *parts = reinterpret_cast<const float *>(a.ws + a.lay.partials);
+  // record of CTA cc's part, query tile i, this thread's row
+  auto rec_of = [&](int cc, int i) {
+    const int sl = 2 * cc + (u0 <= (long long)cc * W / C ? 0 : 1);
+    return parts + ((size_t)sl * 2 + i) * (size_t)kStride * 128 + row;
+  };
+  // query tile i (one at a time; DIFF: the two maps of one head, added into y)
+  const int n_i = DIFF || G >= 2 ? 2 : 1;
+  float y[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) y[e] = 0.f;
+  for (int i = 0; i < n_i; ++i) {
+    const int h = DIFF ? g * G + x : G >= 2 ? g * G + 2 * x + i : g;
+    constexpr int kB = 4;  // parts in flight
+    float M = -INFINITY, L = 0.f;
+    for (int k0 = c1; k0 <= c2; k0 += kB) {
+      float m[kB], l[kB];
+#pragma unroll
+      for (int k = 0; k < kB; ++k) {
+        const float *r = rec_of(min(k0 + k, c2), i);
+        m[k] = k0 + k <= c2 ? __ldcg(r + D * 128) : -INFINITY;
+        l[k] = k0 + k <= c2 ? __ldcg(r + (D + 1) * 128) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < kB; ++k) {
+        const float Mn = fmaxf(M, m[k]);
+        const float fo = M == -INFINITY ? 0.f : exp2_approx(M - Mn);
+        const float fp = m[k] == -INFINITY ? 0.f : exp2_approx(m[k] - Mn);
+        L = __fmaf_rn(l[k], fp, __fmul_rn(L, fo));
+        M = Mn;
+      }
+    }
+    float inv = L > 0.f ? 1.f / L : 0.f;
+    if (DIFF && i == 1) inv *= -__ldg(a.lam + h);
+    if (!DIFF && a.sink && L > 0.f) inv = 1.f / (L + exp2_approx(__ldg(a.sink + h) * kLog2e - M));
+    for (int k0 = c1; k0 <= c2; k0 += kB) {
+      float m[kB], v[kB][E];
+#pragma unroll
+      for (int k = 0; k < kB; ++k) {
+        const float *r = rec_of(min(k0 + k, c2), i);
+        m[k] = k0 + k <= c2 ? __ldcg(r + D * 128) : -INFINITY;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          v[k][e] = k0 + k <= c2 ? __ldcg(r + (w * E + e) * 128) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < kB; ++k) {
+        const float f = m[k] == -INFINITY ? 0.f : exp2_approx(m[k] - M) * inv;
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = __fmaf_rn(v[k][e], f, y[e]);
+      }
+    }
+    if (DIFF && i == 0) continue;
+    float f = 1.f;
+    if (DIFF) {
+      f = a.out_scale;
+      if (a.norm_w) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) ss = __fmaf_rn(y[e], y[e], ss);
+        sq[w][lane] = ss;
+        __syncthreads();
+        ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ss += sq[k][lane];
+        f *= rsqrtf(ss * (1.f / D) + a.eps);
+      }
+    }
+    if (valid) {
+      uint32_t hw[E / 2];
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        float2 wv = make_float2(1.f, 1.f);
+        if (DIFF && a.norm_w)
+          wv = make_float2(__ldg(a.norm_w + w * E + e), __ldg(a.norm_w + w * E + e + 1));
+        const __half2 hv = __floats2half2_rn(y[e] * f * wv.x, y[e + 1] * f * wv.y);
+        hw[e / 2] = *reinterpret_cast<const uint32_t *>(&hv);
+      }
+      uint4 *o = reinterpret_cast<uint4 *>(a.out + (tok * a.Hq + h) * D + w * E);
+#pragma unroll
+      for (int q = 0; q < E / 8; ++q)
+        o[q] = make_uint4(hw[4 * q], hw[4 * q + 1], hw[4 * q + 2], hw[4 * q + 3]);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = 0.f;
+  }
+}
+
 template <int D, int VAR>
 static cudaError_t launch_prefill_t(const AttnArgs &a, int num_sms, const AttnMaps *maps,
                                     cudaStream_t s) {
-  using Cfg = PfCfg<D, VAR == kPfKv8>;
+  using Cfg = PfCfg<D, VAR == kPfKv8, VAR == kPfDiff>;
   static PerDeviceOnce setup;
   if (setup.first()) {
     // setmaxnreg.inc can only draw on registers the block was launched with: refuse to
@@ -1373,7 +1485,18 @@ static cudaError_t launch_prefill_t(const AttnArgs &a, int num_sms, const AttnMa
     setup.mark();
   }
   k_prefill<D, VAR><<<num_sms, kPfThreads, Cfg::kSmem, s>>>(a, *maps);
-  return cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !(VAR == kPfDiff || VAR == kPfWin)) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_sms - 1 > 0 ? num_sms - 1 : 1, 4);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_prefill_join<D, VAR == kPfDiff>, a);
 }
 
 cudaError_t launch_prefill(const AttnArgs &a, int num_sms, const void *tmaps, cudaStream_t s) {

@@ -247,8 +247,8 @@ __device__ __forceinline__ int upper_index(const int *off, int n, long long u, l
 
 __global__ void __launch_bounds__(kPlanThreads, 1)
 k_plan(const int32_t *__restrict__ tpt, int max_pages, const int32_t *__restrict__ kv, int T,
-       int P, int Hkv, int NP, int min_run, int window, bool windowed, int C, unsigned char *ws,
-       WsLayout lay) {
+       int P, int Hkv, int NP, int min_run, int window, bool windowed, bool whole_items, int C,
+       unsigned char *ws, WsLayout lay) {
   __shared__ int sh[32];
   WsHeader *hdr = reinterpret_cast<WsHeader *>(ws);
   int4 *tiles = reinterpret_cast<int4 *>(ws + lay.tiles);
@@ -371,6 +371,9 @@ k_plan(const int32_t *__restrict__ tpt, int max_pages, const int32_t *__restrict
   // decode work goes to min(C, U) CTAs, so that each of them owns at least one unit.
   const long long U = (long long)unit_base * Hkv, W = work_base;
   const int Cd = U < C ? (int)U : C;
+  // whole_items: fewer, longer prefill ranges for a small ubatch, cut at an item's start
+  // where the item is short
+  const int Cp = whole_items ? (int)min((long long)C, max(1ll, W / kPfMinRange)) : C;
   for (int c = tid; c < C; c += kPlanThreads) {
     if (c < Cd) {
       long long u = (long long)c * U / Cd;
@@ -397,26 +400,37 @@ k_plan(const int32_t *__restrict__ tpt, int max_pages, const int32_t *__restrict
       dec_start[4 * c + 2] = make_int4(pg[0], pg[1], pg[2], pg[3]);
       dec_start[4 * c + 3] = make_int4(pg[4], pg[5], pg[6], pg[7]);
     }
-    if (W > 0) {
-      long long w = (long long)c * W / C;
-      int t = upper_index(tile_off, tile_base, w, 1);
-      if (t >= tile_base) t = tile_base - 1;
-      while (tiles[t].z == 0 && t + 1 < tile_base) ++t;
-      int nkb = tiles[t].z;
-      long long r = w - tile_off[t];
-      int j = nkb > 0 ? (int)(r / pf_item_units(nkb)) : 0;
+    if (W > 0 && c < Cp) {
+      // unit w's place: tile, item, key block
+      auto place = [&](long long w) {
+        int t = upper_index(tile_off, tile_base, w, 1);
+        if (t >= tile_base) t = tile_base - 1;
+        while (tiles[t].z == 0 && t + 1 < tile_base) ++t;
+        const int nkb = tiles[t].z;
+        const long long r = w - tile_off[t];
+        const int j = nkb > 0 ? (int)(r / pf_item_units(nkb)) : 0;
+        int kb = nkb > 0 ? (int)(r - (long long)j * pf_item_units(nkb)) : 0;
+        if (whole_items && nkb <= kPfMinItemUnits) kb = 0;
+        return make_int3(t, j, kb);
+      };
+      auto unit_of = [&](int3 p) {
+        return (long long)tile_off[p.x] + (long long)p.y * pf_item_units(tiles[p.x].z) + p.z;
+      };
+      const int3 p0 = place((long long)c * W / Cp);
+      const long long w = unit_of(p0);
       // and the item holding the CTA's last unit, tile * Hkv * NP + item (the prefill
       // kernel runs the segment of that item first, so that both parts of every split
       // item are done early and their combine stays off the end of the launch)
-      long long wl = (long long)(c + 1) * W / C - 1;
+      long long we = (long long)(c + 1) * W / Cp;
+      if (whole_items && c + 1 < Cp) we = unit_of(place(we));
+      long long wl = we - 1;
       if (wl < w) wl = w;
       int tl = upper_index(tile_off, tile_base, wl, 1);
       if (tl >= tile_base) tl = tile_base - 1;
       while (tiles[tl].z == 0 && tl + 1 < tile_base) ++tl;
       const int nkl = tiles[tl].z;
       const int jl = nkl > 0 ? (int)((wl - tile_off[tl]) / pf_item_units(nkl)) : 0;
-      pf_start[c] = make_int4(t, j, nkb > 0 ? (int)(r - (long long)j * pf_item_units(nkb)) : 0,
-                              tl * Hkv * NP + jl);
+      pf_start[c] = make_int4(p0.x, p0.y, p0.z, tl * Hkv * NP + jl);
     }
   }
   if (tid == 0) {
@@ -424,7 +438,7 @@ k_plan(const int32_t *__restrict__ tpt, int max_pages, const int32_t *__restrict
     hdr->n_dec = dec_base;
     hdr->n_units = (int)U;
     hdr->pf_work = work_base;
-    hdr->C = C;
+    hdr->C = Cp;
     hdr->T = T;
     hdr->kind = plan_kind(NP, windowed);
     hdr->Hkv = Hkv;

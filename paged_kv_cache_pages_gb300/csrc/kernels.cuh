@@ -22,8 +22,8 @@ __global__ void k_validate(const int32_t *tpt, int max_pages, const int32_t *kv,
 __global__ void k_plan_mark(const int32_t *tpt, int max_pages, int T, unsigned char *ws,
                             WsLayout lay);
 __global__ void k_plan(const int32_t *tpt, int max_pages, const int32_t *kv, int T, int P, int Hkv,
-                       int NP, int min_run, int window, bool windowed, int C, unsigned char *ws,
-                       WsLayout lay);
+                       int NP, int min_run, int window, bool windowed, bool whole_items, int C,
+                       unsigned char *ws, WsLayout lay);
 
 // Per-device flags of a kernel's one-time launch setup (function attributes are per
 // device).  Returns true for the first caller on the current device, which then

@@ -126,11 +126,15 @@ def test_ragged_chunks_and_single_tokens(pa, min_run, route, P, d, Hq, Hkv, wind
 
 @pytest.mark.gpu
 def test_a_window_past_every_row_is_plain_attention(pa):
-    """The same bits as paged_attn_forward: nothing of the window is left."""
+    """Nothing of the window is left: paged_attn_forward's rows, within the two roundings that
+    each kernel may take (the two plans cut the work at different places)."""
     case = workloads.small_prefill(31, P=32, d=128, Hq=8, Hkv=2, extra_decode=4)
     g, r = whole(pa, case)
     got, _ = check(pa, g, case, r, case.max_pages * case.P)
-    assert torch.equal(got, g.forward(pa))
+    want, tol = ref64.window_attention(case.q, r["kp"], r["vp"], r["tpt"], r["kv"],
+                                       1 / np.sqrt(128), 1 << 30)
+    plain = g.forward(pa).double().cpu().numpy()
+    assert (np.abs(got.double().cpu().numpy() - plain) <= 2 * tol).all()
 
 
 @pytest.mark.gpu
