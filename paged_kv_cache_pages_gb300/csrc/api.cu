@@ -25,6 +25,7 @@ struct NvtxRange {
 };
 
 std::atomic<int> g_min_run{16};
+std::atomic<int> g_least_min_run{16};  // the smallest value that g_min_run has had
 std::atomic<unsigned long long> g_decode_wait_ns{kWaitLimitNs};
 
 int sm_count() {
@@ -533,8 +534,11 @@ static int run_args(const AttnArgs &a, void *stream) {
   int st = encode_attn_maps(a, &maps);
   if (st != PA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = launch_status(launch_prefill(a, sm_count(), &maps, s));
-  if (st != PA_OK) return st;
+  // a ubatch shorter than every threshold that its plan can have been made with has no tile
+  if (a.T >= g_least_min_run.load()) {
+    st = launch_status(launch_prefill(a, sm_count(), &maps, s));
+    if (st != PA_OK) return st;
+  }
   return launch_status(launch_decode(a, sm_count(), &maps, s));
 }
 
@@ -680,6 +684,9 @@ unsigned long long paged_attn_set_decode_wait_limit(unsigned long long ns) {
 
 int paged_attn_set_prefill_min_run(int min_run) {
   if (min_run < 1) min_run = 1;
+  int least = g_least_min_run.load();
+  while (min_run < least && !g_least_min_run.compare_exchange_weak(least, min_run)) {
+  }
   return g_min_run.exchange(min_run);
 }
 

@@ -1131,9 +1131,20 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       // P as the A fragment of the PV product (k = the warp's 16 keys; rows 8..15: the
       // second map, else zero)
       uint32_t pa0, pa2, pa1 = 0u, pa3 = 0u;
+      // DIFF: what binary16 leaves of P goes through a second product.  The difference of two
+      // maps cancels, so that P's rounding weighs more than in one map (1.5 times the error of
+      // the output's own rounding; with the rest, 1.0); the launch waits for its bytes anyway.
+      uint32_t pr[4] = {0u, 0u, 0u, 0u};
       if constexpr (DIFF) {
         pa1 = pack_h2(p[1][0], p[1][1]);
         pa3 = pack_h2(p[1][2], p[1][3]);
+#pragma unroll
+        for (int r = 0; r < NM; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            const float2 h = h2_to_f2(pack_h2(p[r][j], p[r][j + 1]));
+            pr[r + j] = pack_h2(p[r][j] - h.x, p[r][j + 1] - h.y);
+          }
       }
       if (KV8) {
         // fold each key's V scale into P (a key past the valid ones contributes 0)
@@ -1223,6 +1234,10 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           ldsm_x4_t(sV + box * kBox + sw128(lt_key, chunk), b0, b1, b2, b3);
           mma16816(o[t], pa0, pa1, pa2, pa3, b0, b1);
           mma16816(o[t + 1], pa0, pa1, pa2, pa3, b2, b3);
+          if (DIFF) {
+            mma16816(o[t], pr[0], pr[1], pr[2], pr[3], b0, b1);
+            mma16816(o[t + 1], pr[0], pr[1], pr[2], pr[3], b2, b3);
+          }
         }
       }
     }

@@ -917,9 +917,11 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         const int h = !DIFF && wg ? w.h1 : w.h0;
         const int tok = w.tile_start + row;
         const bool valid = row < w.n_tok;
-        if (w.tile != l_tile) L = valid ? min(max(a.kv[tok], 0), cap) : 0;
+        // (rows past the tile's tokens count as seeing every key, so that a short tile's whole
+        // blocks need no mask; they are never stored)
+        if (w.tile != l_tile) L = valid ? min(max(a.kv[tok], 0), cap) : MASK ? 0 : w.max_kv;
         l_tile = w.tile;
-        const int lo = WIN ? max(L - window, 0) : 0;  // first visible key
+        const int lo = WIN && valid ? max(L - window, 0) : 0;  // first visible key
         // masked variant: this row's (sequence, position); -2 matches no cell
         const int my_seq = MASK && valid ? a.tok_seq[tok] : -2;
         const int my_pos = MASK && valid ? a.tok_pos[tok] : -1;
@@ -995,8 +997,17 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
             for (int j = 0; j < 128; ++j)
               t[j] = (mw[j >> 5] >> (j & 31)) & 1u ? t[j] : 0xff800000u;
           } else if (!wfull) {
+            // the visible keys as bits: a column costs a select and part of a bit test instead of
+            // one or two compares (windowed tiles, all of whose blocks are cut: 78 to 63 us)
 #pragma unroll
-            for (int j = 0; j < 128; ++j) t[j] = j < nv && (!WIN || j >= nlo) ? t[j] : 0xff800000u;  // -inf
+            for (int q = 0; q < 4; ++q) {
+              const int hi = min(max(nv - 32 * q, 0), 32), lw = min(max(nlo - 32 * q, 0), 32);
+              uint32_t m = (uint32_t)((1ull << hi) - 1);
+              if (WIN) m &= ~(uint32_t)((1ull << lw) - 1);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                t[32 * q + j] = (m & (1u << j)) ? t[32 * q + j] : 0xff800000u;  // -inf
+            }
           }
           float mx = -INFINITY;
 #pragma unroll
