@@ -28,9 +28,9 @@
  *              pa_pool_fork (copy-on-write forks of shared pages)
  *  other attentions over the same pages:  paged_attn_diff_workspace_size,
  *              paged_attn_plan_diff, paged_attn_diff_run, paged_attn_diff_forward
- *              (differential attention); paged_attn_plan_window,
- *              paged_attn_window_run, paged_attn_window_forward (a window over
- *              the last positions, with sinks)
+ *              (differential attention); paged_attn_window_workspace_size,
+ *              paged_attn_plan_window, paged_attn_window_run,
+ *              paged_attn_window_forward (a window over the last positions, with sinks)
  *
  * Conventions shared by every call
  * --------------------------------
@@ -493,12 +493,14 @@ int paged_attn_diff_forward(const uint16_t *q, const uint16_t *k_pages, const ui
  * are consecutive and have identical rows): such pages may have been given back.  Cells
  * before a window never reach the output, whatever they hold.
  *
- * paged_attn_plan_window plans with a window (workspace as paged_attn_workspace_size; one
- * plan serves every layer with that window); paged_attn_window_run runs on it, with the
+ * paged_attn_plan_window plans with a window (in a workspace of
+ * paged_attn_window_workspace_size bytes; one plan serves every layer with that window);
+ * paged_attn_window_run runs on it, with the
  * plan's window, and on another plan sets PA_ERR_PLAN and writes nothing.  The plain run and
  * its prefill refuse a windowed plan in the same way.  paged_attn_window_forward is the plan
  * followed by the run.
  */
+size_t paged_attn_window_workspace_size(int T, int Hq, int Hkv, int d);
 int paged_attn_plan_window(const int32_t *tok_page_table, int max_pages,
                            const int32_t *tok_kv_len, int T, int Hq, int Hkv, int P, int d,
                            int window, void *workspace, size_t workspace_bytes, void *stream);

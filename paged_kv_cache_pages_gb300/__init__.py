@@ -94,6 +94,7 @@ _SIGS = {
     "paged_attn_plan_diff": ([_vp, _i, _vp, _i, _i, _i, _i, _i, _vp, _sz, _vp], _i),
     "paged_attn_diff_run": (_ATTN_ARGS[:13] + [_vp, _vp, _f, _f] + _ATTN_ARGS[13:], _i),
     "paged_attn_diff_forward": (_ATTN_ARGS[:13] + [_vp, _vp, _f, _f] + _ATTN_ARGS[13:], _i),
+    "paged_attn_window_workspace_size": ([_i, _i, _i, _i], _sz),
     "paged_attn_plan_window": ([_vp, _i, _vp, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp], _i),
     "paged_attn_window_run": (_ATTN_ARGS[:13] + [_vp] + _ATTN_ARGS[13:], _i),
     "paged_attn_window_forward": (_ATTN_ARGS[:13] + [_i, _vp] + _ATTN_ARGS[13:], _i),
@@ -172,8 +173,13 @@ def workspace_size(T: int, Hq: int, Hkv: int, d: int) -> int:
     return int(_lib.paged_attn_workspace_size(T, Hq, Hkv, d))
 
 
+def window_workspace_size(T: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(_lib.paged_attn_window_workspace_size(T, Hq, Hkv, d))
+
+
 def new_workspace(T: int, Hq: int, Hkv: int, d: int, device=None) -> torch.Tensor:
-    n = workspace_size(T, Hq, Hkv, d)
+    """Workspace of every call for these shapes but the differential ones (new_diff_workspace)."""
+    n = max(workspace_size(T, Hq, Hkv, d), window_workspace_size(T, Hq, Hkv, d))
     if n == 0:
         raise PagedAttnError(PA_EUNSUPPORTED, "workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")

@@ -58,11 +58,11 @@ int check_shape(int Hq, int Hkv, int P, int d) {
 int launch_status(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ELAUNCH; }
 
 // Common checks of the attention calls.  maps: softmax maps per query head (the workspace
-// counts a head once per map).
+// counts a head once per map); both: the workspace of a kind whose two launches run side by side.
 int check_attn(const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
                const int32_t *tpt, int max_pages, const int32_t *kv, int T, int Hq, int Hkv, int P,
                int d, int num_pages, const uint16_t *out, const void *ws, size_t ws_bytes,
-               bool need_data, int maps = 1) {
+               bool need_data, int maps = 1, bool both = false) {
   if (T < 0 || max_pages < 0 || num_pages < 0) return PA_EINVAL;
   int st = check_shape(Hq, Hkv, P, d);
   if (st != PA_OK) return st;
@@ -74,7 +74,8 @@ int check_attn(const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pag
   if (!ws) return PA_EWORKSPACE;
   int C = sm_count();
   if (C <= 0) return PA_ELAUNCH;
-  if (ws_bytes < ws_layout(T, Hq * maps, Hkv, d, C).total) return PA_EWORKSPACE;
+  if (both && C > kJoinScratchParts) return PA_EUNSUPPORTED;
+  if (ws_bytes < ws_layout(T, Hq * maps, Hkv, d, C, both).total) return PA_EWORKSPACE;
   if (!aligned16(ws) || !aligned16(tpt) || !aligned16(kv)) return PA_EALIGN;
   if (need_data && (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out)))
     return PA_EALIGN;
@@ -109,7 +110,7 @@ AttnArgs make_args(const uint16_t *q, const uint16_t *k_pages, const uint16_t *v
   a.lam = a.norm_w = a.sink = nullptr;
   a.eps = 0.f;
   a.out_scale = 1.f;
-  a.windowed = false;
+  a.windowed = a.overlap = false;
   return a;
 }
 
@@ -340,11 +341,12 @@ static int plan_with(const int32_t *tok_page_table, int max_pages, const int32_t
                      size_t workspace_bytes, void *stream, int min_run, int maps, bool windowed,
                      int window) {
   int st = check_attn(nullptr, nullptr, nullptr, tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv,
-                      P, d, 1, nullptr, workspace, workspace_bytes, false, maps);
+                      P, d, 1, nullptr, workspace, workspace_bytes, false, maps,
+                      windowed || maps > 1);
   if (st != PA_OK) return st;
   if (T == 0) return PA_OK;
   const int C = sm_count();
-  WsLayout lay = ws_layout(T, Hq * maps, Hkv, d, C);
+  WsLayout lay = ws_layout(T, Hq * maps, Hkv, d, C, windowed || maps > 1);
   const int G = Hq * maps / Hkv;
   const int NP = G >= 2 ? G / 2 : 1;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -513,11 +515,19 @@ int paged_attn_forward(const uint16_t *q, const uint16_t *k_pages, const uint16_
                         d, num_pages, scale, out, workspace, workspace_bytes, stream);
 }
 
-size_t paged_attn_diff_workspace_size(int T, int Hq, int Hkv, int d) {
+static size_t both_size(int T, int Hq, int Hkv, int d, int maps) {
   if (T < 0 || check_shape(Hq, Hkv, 16, d) != PA_OK) return 0;
   int C = sm_count();
   if (C <= 0) C = 256;  // no device visible: as paged_attn_workspace_size
-  return ws_layout(T, Hq * kDiffMaps, Hkv, d, C).total;
+  return ws_layout(T, Hq * maps, Hkv, d, C, true).total;
+}
+
+size_t paged_attn_diff_workspace_size(int T, int Hq, int Hkv, int d) {
+  return both_size(T, Hq, Hkv, d, kDiffMaps);
+}
+
+size_t paged_attn_window_workspace_size(int T, int Hq, int Hkv, int d) {
+  return both_size(T, Hq, Hkv, d, 1);
 }
 
 int paged_attn_plan_diff(const int32_t *tok_page_table, int max_pages, const int32_t *tok_kv_len,
@@ -528,14 +538,16 @@ int paged_attn_plan_diff(const int32_t *tok_page_table, int max_pages, const int
                    workspace_bytes, stream, g_min_run.load(), kDiffMaps);
 }
 
-// Prefill tiles, then decode tokens, of a planned ubatch whose arguments are in `a`.
-static int run_args(const AttnArgs &a, void *stream) {
+// Prefill tiles and, beside them, decode tokens of a planned ubatch whose arguments are in `a`
+// (the second launch also joins the parts of the first one's split items).
+static int run_args(AttnArgs &a, void *stream) {
   AttnMaps maps;
   int st = encode_attn_maps(a, &maps);
   if (st != PA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // a ubatch shorter than every threshold that its plan can have been made with has no tile
-  if (a.T >= g_least_min_run.load()) {
+  a.overlap = a.T >= g_least_min_run.load();
+  if (a.overlap) {
     st = launch_status(launch_prefill(a, sm_count(), &maps, s));
     if (st != PA_OK) return st;
   }
@@ -551,12 +563,12 @@ static int diff_setup(const uint16_t *q, const uint16_t *k_pages, const uint16_t
                       const float *lam, const float *norm_weight, float eps, float out_scale,
                       uint16_t *out, void *workspace, size_t workspace_bytes, AttnArgs *a) {
   int st = check_attn(q, k_pages, v_pages, tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P, d,
-                      num_pages, out, workspace, workspace_bytes, true, kDiffMaps);
+                      num_pages, out, workspace, workspace_bytes, true, kDiffMaps, true);
   if (st != PA_OK || T == 0) return st;
   if (!lam || !good_scale(scale) || (norm_weight && !(eps >= 0.f))) return PA_EINVAL;
   *a = make_args(q, k_pages, v_pages, tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P, d,
                  num_pages, scale, out, workspace);
-  a->lay = ws_layout(T, Hq * kDiffMaps, Hkv, d, sm_count());
+  a->lay = ws_layout(T, Hq * kDiffMaps, Hkv, d, sm_count(), true);
   a->lam = lam;
   a->norm_w = norm_weight;
   a->eps = eps;
@@ -611,11 +623,12 @@ static int window_setup(const uint16_t *q, const uint16_t *k_pages, const uint16
                         const float *sink, uint16_t *out, void *workspace, size_t workspace_bytes,
                         AttnArgs *a) {
   int st = check_attn(q, k_pages, v_pages, tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P, d,
-                      num_pages, out, workspace, workspace_bytes, true);
+                      num_pages, out, workspace, workspace_bytes, true, 1, true);
   if (st != PA_OK || T == 0) return st;
   if (!good_scale(scale)) return PA_EINVAL;
   *a = make_args(q, k_pages, v_pages, tok_page_table, max_pages, tok_kv_len, T, Hq, Hkv, P, d,
                  num_pages, scale, out, workspace);
+  a->lay = ws_layout(T, Hq, Hkv, d, sm_count(), true);
   a->windowed = true;
   a->sink = sink;
   return PA_OK;

@@ -27,6 +27,9 @@ namespace pa {
 //                                  then the page ids of that unit's key block (8 ints, -1 past its end)
 //   pf_start       int4 [C]      first prefill unit of each CTA: (tile, item in tile, kb,
 //                                  tile * items per tile + item of the CTA's last unit)
+//   pf_split       int4 [C]      (differential and windowed plans) the prefill items that are
+//                                  cut over CTAs: (tile, 2 item + slot of the first part's
+//                                  record, first CTA, parts)
 //   pf_cnt         int  [T * Hkv * NP * 2 * 4]  arrival counters of split prefill items,
 //                                  one per (item, softmax warpgroup, warp)
 //   dec_cnt        int  [T * Hkv]   arrival counters of decode segments split over CTAs
@@ -34,7 +37,8 @@ namespace pa {
 //                    decode split partials  float [(T*Hkv + C)][G][D + 2]
 //                    prefill split parts    float [2C][2][128][D + 4]  (16-byte rows)
 // The decode and prefill kernels of one ubatch run one after the other on a
-// stream, so their partials share one region.
+// stream, so their partials share one region.  (The differential and windowed ones run
+// side by side: `both` gives the decode partials a region behind the prefill's.)
 // ----------------------------------------------------------------------------
 struct WsHeader {
   int err;        // PA_ERR_* bits
@@ -48,7 +52,10 @@ struct WsHeader {
   int Hkv;
   int window;     // windowed plan: positions a token attends to (INT_MAX: all)
   int P, max_pages;
-  int pad[52];
+  int C_dec;      // CTAs that the decode units were cut for
+  int n_split;    // entries of pf_split
+  int many_parts; // whether one of them has more than kJoinFewParts parts
+  int pad[49];
 };
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 
@@ -75,16 +82,22 @@ __host__ __device__ inline int pf_item_units(int nkb) {
 // CTAs instead of to parts of a block each.
 constexpr int kPfMinRange = 4;
 
+// Parts of a split prefill item that the join's scratch holds for one unit of its work, and for
+// each of four (an item has at most one part per SM).
+constexpr int kJoinScratchParts = 256, kJoinFewParts = kJoinScratchParts / 4;
+
 struct WsLayout {
-  size_t tiles, dec_tok, tok_unit_off, flags, runs, tile_off, dec_start, pf_start, pf_cnt;
+  size_t tiles, dec_tok, tok_unit_off, flags, runs, tile_off, dec_start, pf_start, pf_split;
+  size_t pf_cnt;
   size_t dec_cnt;
-  size_t partials, total;
+  size_t partials, dec_partials, total;
   int n_cnt;  // entries of pf_cnt
 };
 
 __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-__host__ __device__ inline WsLayout ws_layout(int T, int Hq, int Hkv, int D, int C) {
+__host__ __device__ inline WsLayout ws_layout(int T, int Hq, int Hkv, int D, int C,
+                                              bool both = false) {
   WsLayout l;
   size_t o = sizeof(WsHeader);
   size_t Tm = T > 0 ? (size_t)T : 1;
@@ -98,14 +111,17 @@ __host__ __device__ inline WsLayout ws_layout(int T, int Hq, int Hkv, int D, int
   l.tile_off = o;     o = align_up(o + (Tm + 1) * 4, 256);
   l.dec_start = o;    o = align_up(o + (size_t)C * 64, 256);
   l.pf_start = o;     o = align_up(o + (size_t)C * 16, 256);
+  l.pf_split = o;     if (both) o = align_up(o + (size_t)C * 16, 256);
   l.n_cnt = (int)(Tm * Hkv * NP * 8);
   l.pf_cnt = o;       o = align_up(o + (size_t)l.n_cnt * 4, 256);
   l.dec_cnt = o;      o = align_up(o + Tm * Hkv * 4, 256);
   l.partials = o;
   size_t dec_part = (Tm * Hkv + (size_t)C) * G * (D + 2) * 4;
   size_t pf_part = (size_t)2 * C * 2 * 128 * (D + 4) * 4;
-  o = align_up(o + (dec_part > pf_part ? dec_part : pf_part), 256);
-  l.total = o;
+  l.dec_partials = both ? align_up(o + pf_part, 256) : o;
+  size_t end = l.dec_partials + dec_part;
+  if (!both && o + pf_part > end) end = o + pf_part;
+  l.total = align_up(end, 256);
   return l;
 }
 

@@ -44,6 +44,7 @@
 //
 // WIN: the plan lays out only the blocks from the one that holds a token's first visible
 // key, so the bytes before the window are never read.
+#include "join.cuh"
 #include "kernels.cuh"
 #include "tc.cuh"
 #include "tmap.cuh"
@@ -511,11 +512,16 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       }
     }
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // DIFF, WIN behind this run's prefill (a.overlap): everything that the decode tokens need was
+  // done before the prefill began, so this launch runs beside it, on the SMs that the prefill
+  // leaves (a step of 76 tokens: 31 to 24 us), and waits for it only before it joins the
+  // prefill's split items.
+  const bool late = (DIFF || WIN) && a.overlap;
+  WsHeader *hdr = reinterpret_cast<WsHeader *>(a.ws);
+  if (!late) asm volatile("griddepcontrol.wait;" ::: "memory");
   // the next kernel in the stream may be scheduled onto SMs as this grid's CTAs leave
   // them (a programmatically launched successor still waits for this grid to complete)
   asm volatile("griddepcontrol.launch_dependents;");
-  WsHeader *hdr = reinterpret_cast<WsHeader *>(a.ws);
   const int c = blockIdx.x;
   // Everything the first copy needs is loaded here, at once, so that it costs one L2
   // round trip after the wait rather than a chain of dependent ones: the header's
@@ -527,10 +533,12 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
     const int want = DIFF ? plan_kind(G, false) : plan_kind(G >= 2 ? G / 2 : 1, true);
     if (__ldcg(&hdr->kind) != want) {
       if (tid == 0 && blockIdx.x == 0) atomicOr(&hdr->err, PA_ERR_PLAN);
+      if (late) asm volatile("griddepcontrol.wait;" ::: "memory");
       return;
     }
   }
   const int window = WIN ? __ldcg(&hdr->window) : 0;
+  const int c_dec = DIFF || WIN ? __ldcg(&hdr->C_dec) : 0;
   const int4 *start = reinterpret_cast<const int4 *>(a.ws + a.lay.dec_start) + 4 * c;
   int4 start0 = make_int4(0, 0, 0, 0), start1 = start0, start2 = start0, start3 = start0;
   if (w == kDecWarps) {
@@ -550,7 +558,7 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   v.kv = a.kv;
   v.tok_seq = MASK ? a.tok_seq : nullptr;
   v.tok_pos = MASK ? a.tok_pos : nullptr;
-  float *partials = reinterpret_cast<float *>(a.ws + a.lay.partials);
+  float *partials = reinterpret_cast<float *>(a.ws + a.lay.dec_partials);
   int *dec_cnt = reinterpret_cast<int *>(a.ws + a.lay.dec_cnt);
 
   const int U = counts.y;
@@ -563,11 +571,17 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       for (int x = lane; x < a.Hq * D; x += 32) orow[x] = 0;
     }
   }
-  // the units go to C = min(gridDim.x, U) CTAs, each of which owns at least one
-  const int C = min((int)gridDim.x, U);
-  if (c >= C) return;
-  const int u0 = (int)((int64_t)c * U / C), u1 = (int)((int64_t)(c + 1) * U / C);
-  if (u0 >= u1) return;
+  // the units go to C = min(gridDim.x, U) CTAs (DIFF, WIN: as many as the plan says), each of
+  // which owns at least one
+  const int C = DIFF || WIN ? min((int)gridDim.x, c_dec) : min((int)gridDim.x, U);
+  const int u0 = c < C ? (int)((int64_t)c * U / C) : 0;
+  const int u1 = c < C ? (int)((int64_t)(c + 1) * U / C) : 0;
+  if (u0 >= u1) {
+    if constexpr (DIFF || WIN) {
+      if (late && w < kDecWarps) join_items<D, DIFF>(a, hdr, smem);
+    }
+    return;
+  }
   const int n = u1 - u0;
 
   volatile int *abort = &bars->abort;
@@ -1451,6 +1465,20 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
     if (dec_wait(&bars->job_empty[q], ((n_jobs / kJobs) & 1) ^ 1, err, abort, a.wait_ns)) {
       bars->jobs[q].ig = -1;
       mbar_arrive(&bars->job_full[q]);
+    }
+  }
+  if constexpr (DIFF || WIN) {
+    if (late) {
+      // the ring is free: every stage that was issued has been consumed (not after giving up,
+      // which one thread decides for all: they meet at barriers)
+      consumers_sync();
+      if (tid == 0) bars->last = *abort ? 0 : 1;
+      consumers_sync();
+      static_assert(NS * Cfg::kStage >= kJoinScratch, "the join's scratch");
+      if (*reinterpret_cast<volatile int *>(&bars->last))
+        join_items<D, DIFF>(a, hdr, smem);
+      else
+        asm volatile("griddepcontrol.wait;" ::: "memory");
     }
   }
 }

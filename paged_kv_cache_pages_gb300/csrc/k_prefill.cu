@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   constexpr bool MASK = VAR == kPfMask, KV8 = VAR == kPfKv8;
   constexpr bool DIFF = VAR == kPfDiff, WIN = VAR == kPfWin;
-  constexpr bool JOIN = DIFF || WIN;  // split items are joined by k_prefill_join
+  constexpr bool JOIN = DIFF || WIN;  // split items are joined by the split-KV launch (join.cuh)
   constexpr int kItemHeads = DIFF ? 1 : 2;
   static_assert(!KV8 || D == 128, "FP8 pages: d 128");
   using Cfg = PfCfg<D, KV8, DIFF>;
@@ -577,8 +577,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = hdr->C;
   const int c = blockIdx.x;
-  // the join behind this kernel may take the SMs that this grid's CTAs leave (it waits for the
-  // whole grid before it reads anything)
+  // the split-KV launch behind this one may take the SMs that this grid leaves
   if (JOIN) asm volatile("griddepcontrol.launch_dependents;");
   if (c >= C) return;
   if (hdr->kind != plan_kind(NP, WIN)) {  // the tile records are another operator's
@@ -1207,7 +1206,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           tc::fence_before_sync();
           mbar_arrive(&bars->o_empty[wg]);
           if (DIFF) mbar_arrive(&bars->o_empty[wg ^ 1]);  // this warpgroup does not read it
-          if (JOIN) {  // k_prefill_join folds the parts
+          if (JOIN) {  // the split-KV launch behind this one folds the parts
             sc += nseg;
             ++nitem;
             continue;
@@ -1361,123 +1360,6 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   }
 }
 
-// The parts of the split items of a differential (DIFF) or windowed plan, folded into the
-// output.  The item cut by CTA c's first unit, if CTA c - 1 holds its first key block, is CTA
-// c's to join, 32 of its rows to each CTA of the column; a thread has one row (a warp's reads of
-// one element of 32 rows are one line) and D / 8 of its values.  As a launch of its own, any
-// number of parts is read at the rate of the whole GPU: the last part's softmax warps took 70 us
-// for ten parts (an L2 round trip at a time), and their code cost the whole blocks registers.
-template <int D, bool DIFF>
-__global__ void __launch_bounds__(256) k_prefill_join(AttnArgs a) {
-  constexpr int NM = DIFF ? 2 : 1, E = D / 8, kStride = D + 4;
-  __shared__ float sq[8][32];
-  asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const WsHeader *hdr = reinterpret_cast<const WsHeader *>(a.ws);
-  const int G = a.Hq / a.Hkv, NP = DIFF ? G : G >= 2 ? G / 2 : 1;
-  const int C = hdr->C, c = blockIdx.x + 1;
-  const long long W = hdr->pf_work;
-  if (hdr->kind != plan_kind(NP, !DIFF) || c >= C || W <= 0) return;
-  const int4 st = reinterpret_cast<const int4 *>(a.ws + a.lay.pf_start)[c];  // tile, item, block
-  if (st.z == 0) return;  // the range starts at an item's start
-  const int4 tl = reinterpret_cast<const int4 *>(a.ws + a.lay.tiles)[st.x];
-  const long long u0 = (long long)reinterpret_cast<const int *>(a.ws + a.lay.tile_off)[st.x] +
-                       (long long)st.y * pf_item_units(tl.z);
-  const int c1 = cta_of_unit(u0, W, C), c2 = cta_of_unit(u0 + tl.z - 1, W, C);
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int n_tok = tl.y & 0xffff, row = blockIdx.y * 32 + lane;
-  if (c1 != c - 1 || blockIdx.y * 32 >= n_tok) return;
-  const int g = st.y / NP, x = st.y - g * NP;
-  const bool valid = row < n_tok;
-  const size_t tok = (size_t)(tl.x + min(row, n_tok - 1));
-  const float *parts = reinterpret_cast<const float *>(a.ws + a.lay.partials);
-  // record of CTA cc's part, query tile i, this thread's row
-  auto rec_of = [&](int cc, int i) {
-    const int sl = 2 * cc + (u0 <= (long long)cc * W / C ? 0 : 1);
-    return parts + ((size_t)sl * 2 + i) * (size_t)kStride * 128 + row;
-  };
-  // query tile i (one at a time; DIFF: the two maps of one head, added into y)
-  const int n_i = DIFF || G >= 2 ? 2 : 1;
-  float y[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) y[e] = 0.f;
-  for (int i = 0; i < n_i; ++i) {
-    const int h = DIFF ? g * G + x : G >= 2 ? g * G + 2 * x + i : g;
-    constexpr int kB = 4;  // parts in flight
-    float M = -INFINITY, L = 0.f;
-    for (int k0 = c1; k0 <= c2; k0 += kB) {
-      float m[kB], l[kB];
-#pragma unroll
-      for (int k = 0; k < kB; ++k) {
-        const float *r = rec_of(min(k0 + k, c2), i);
-        m[k] = k0 + k <= c2 ? __ldcg(r + D * 128) : -INFINITY;
-        l[k] = k0 + k <= c2 ? __ldcg(r + (D + 1) * 128) : 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < kB; ++k) {
-        const float Mn = fmaxf(M, m[k]);
-        const float fo = M == -INFINITY ? 0.f : exp2_approx(M - Mn);
-        const float fp = m[k] == -INFINITY ? 0.f : exp2_approx(m[k] - Mn);
-        L = __fmaf_rn(l[k], fp, __fmul_rn(L, fo));
-        M = Mn;
-      }
-    }
-    float inv = L > 0.f ? 1.f / L : 0.f;
-    if (DIFF && i == 1) inv *= -__ldg(a.lam + h);
-    if (!DIFF && a.sink && L > 0.f) inv = 1.f / (L + exp2_approx(__ldg(a.sink + h) * kLog2e - M));
-    for (int k0 = c1; k0 <= c2; k0 += kB) {
-      float m[kB], v[kB][E];
-#pragma unroll
-      for (int k = 0; k < kB; ++k) {
-        const float *r = rec_of(min(k0 + k, c2), i);
-        m[k] = k0 + k <= c2 ? __ldcg(r + D * 128) : -INFINITY;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          v[k][e] = k0 + k <= c2 ? __ldcg(r + (w * E + e) * 128) : 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < kB; ++k) {
-        const float f = m[k] == -INFINITY ? 0.f : exp2_approx(m[k] - M) * inv;
-#pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = __fmaf_rn(v[k][e], f, y[e]);
-      }
-    }
-    if (DIFF && i == 0) continue;
-    float f = 1.f;
-    if (DIFF) {
-      f = a.out_scale;
-      if (a.norm_w) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) ss = __fmaf_rn(y[e], y[e], ss);
-        sq[w][lane] = ss;
-        __syncthreads();
-        ss = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) ss += sq[k][lane];
-        f *= rsqrtf(ss * (1.f / D) + a.eps);
-      }
-    }
-    if (valid) {
-      uint32_t hw[E / 2];
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        float2 wv = make_float2(1.f, 1.f);
-        if (DIFF && a.norm_w)
-          wv = make_float2(__ldg(a.norm_w + w * E + e), __ldg(a.norm_w + w * E + e + 1));
-        const __half2 hv = __floats2half2_rn(y[e] * f * wv.x, y[e + 1] * f * wv.y);
-        hw[e / 2] = *reinterpret_cast<const uint32_t *>(&hv);
-      }
-      uint4 *o = reinterpret_cast<uint4 *>(a.out + (tok * a.Hq + h) * D + w * E);
-#pragma unroll
-      for (int q = 0; q < E / 8; ++q)
-        o[q] = make_uint4(hw[4 * q], hw[4 * q + 1], hw[4 * q + 2], hw[4 * q + 3]);
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = 0.f;
-  }
-}
-
 template <int D, int VAR>
 static cudaError_t launch_prefill_t(const AttnArgs &a, int num_sms, const AttnMaps *maps,
                                     cudaStream_t s) {
@@ -1496,18 +1378,7 @@ static cudaError_t launch_prefill_t(const AttnArgs &a, int num_sms, const AttnMa
     setup.mark();
   }
   k_prefill<D, VAR><<<num_sms, kPfThreads, Cfg::kSmem, s>>>(a, *maps);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !(VAR == kPfDiff || VAR == kPfWin)) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(num_sms - 1 > 0 ? num_sms - 1 : 1, 4);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_prefill_join<D, VAR == kPfDiff>, a);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_prefill(const AttnArgs &a, int num_sms, const void *tmaps, cudaStream_t s) {

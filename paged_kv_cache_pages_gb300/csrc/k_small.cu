@@ -370,10 +370,12 @@ k_plan(const int32_t *__restrict__ tpt, int max_pages, const int32_t *__restrict
   // 6. where each of the C CTAs starts in the decode and in the prefill work.  The
   // decode work goes to min(C, U) CTAs, so that each of them owns at least one unit.
   const long long U = (long long)unit_base * Hkv, W = work_base;
-  const int Cd = U < C ? (int)U : C;
   // whole_items: fewer, longer prefill ranges for a small ubatch, cut at an item's start
-  // where the item is short
+  // where the item is short; and if they leave half of the SMs, the decode tokens' launch,
+  // which then runs beside them, goes to the SMs that are left
   const int Cp = whole_items ? (int)min((long long)C, max(1ll, W / kPfMinRange)) : C;
+  const int Cmax = whole_items && W > 0 && Cp <= C / 2 ? C - Cp : C;
+  const int Cd = U < Cmax ? (int)U : Cmax;
   for (int c = tid; c < C; c += kPlanThreads) {
     if (c < Cd) {
       long long u = (long long)c * U / Cd;
@@ -433,12 +435,44 @@ k_plan(const int32_t *__restrict__ tpt, int max_pages, const int32_t *__restrict
       pf_start[c] = make_int4(p0.x, p0.y, p0.z, tl * Hkv * NP + jl);
     }
   }
+  // 7. the items that the prefill's cuts divide, at the first cut of each
+  if (whole_items) {
+    __syncthreads();
+    int4 *split = reinterpret_cast<int4 *>(ws + lay.pf_split);
+    int n_split = 0, many = 0;
+    for (int c0 = 1; c0 < Cp; c0 += kPlanThreads) {
+      const int c = c0 + tid;
+      int4 e = make_int4(0, 0, 0, 0);
+      bool cut = false;
+      if (c < Cp && W > 0) {
+        const int4 st = pf_start[c];
+        if (st.z > 0) {
+          const long long u0 =
+              (long long)tile_off[st.x] + (long long)st.y * pf_item_units(tiles[st.x].z);
+          const int c1 = cta_of_unit(u0, W, Cp);
+          cut = c1 == c - 1;
+          e = make_int4(st.x, 2 * st.y + (u0 <= (long long)c1 * W / Cp ? 0 : 1), c1,
+                        cta_of_unit(u0 + tiles[st.x].z - 1, W, Cp) - c1 + 1);
+        }
+      }
+      int tot;
+      const int at = block_excl_scan(cut ? 1 : 0, &tot, sh) + n_split;
+      if (cut) split[at] = e;
+      n_split += tot;
+      many |= __syncthreads_or(cut && e.w > kJoinFewParts);
+    }
+    if (tid == 0) {
+      hdr->n_split = n_split;
+      hdr->many_parts = many;
+    }
+  }
   if (tid == 0) {
     hdr->n_tiles = tile_base;
     hdr->n_dec = dec_base;
     hdr->n_units = (int)U;
     hdr->pf_work = work_base;
     hdr->C = Cp;
+    hdr->C_dec = Cd;
     hdr->T = T;
     hdr->kind = plan_kind(NP, windowed);
     hdr->Hkv = Hkv;

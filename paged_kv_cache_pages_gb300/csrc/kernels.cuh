@@ -75,6 +75,9 @@ struct AttnArgs {
   // logit of every query head [Hq] (null: none)
   bool windowed;
   const float *sink;
+  // differential and windowed split-KV launches: the launch before is this run's prefill, whose
+  // tiles need not be done for the decode tokens, and whose split items this launch joins
+  bool overlap;
 };
 
 // Differential attention reads a cached K row as two keys (k1 | k2) of d / 2 and a query row
