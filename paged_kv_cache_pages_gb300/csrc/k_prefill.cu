@@ -88,11 +88,19 @@ struct PfBars {
   uint64_t k_full[kPfStages], k_empty[kPfStages], v_full[kPfStages], v_empty[kPfStages];
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint64_t turn[2];  // issuer turns: tile 1's issuer -> tile 0's, tile 0's -> tile 1's
-  // FP8 pages: a block's codes have landed (K, V); the V scales of the stage's block are in
-  uint64_t kc_full, vc_full;
-  uint64_t vs_full[kPfStages];
-  // DIFF: a warpgroup's row sums, then its sums of squares, are in shared memory
-  uint64_t xl_full[2], xs_full[2];
+  union {
+    struct {
+      // FP8 pages: a block's codes have landed (K, V); the V scales of the stage's block are in
+      uint64_t kc_full, vc_full;
+      uint64_t vs_full[kPfStages];
+    };
+    struct {
+      // WIN: P of the block's first 64 keys is in TMEM
+      uint64_t p_half[2];
+      // DIFF: a warpgroup's row sums, then its sums of squares, are in shared memory
+      uint64_t xl_full[2], xs_full[2];
+    };
+  };
   uint32_t tmem_base;
   int abort;
 };
@@ -557,6 +565,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   constexpr bool MASK = VAR == kPfMask, KV8 = VAR == kPfKv8;
   constexpr bool DIFF = VAR == kPfDiff, WIN = VAR == kPfWin;
+  // The products of a block's first 64 keys start while the softmax computes the other half of
+  // P.  Measured: windowed chunks 138 to 127 us; differential ones, whose blocks have fewer MMAs
+  // to hide behind the second hand-off, 413 to 421 us, so they keep one.
+  constexpr bool HALF = WIN;
   constexpr bool JOIN = DIFF || WIN;  // split items are joined by the split-KV launch (join.cuh)
   constexpr int kItemHeads = DIFF ? 1 : 2;
   static_assert(!KV8 || D == 128, "FP8 pages: d 128");
@@ -610,16 +622,21 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
     }
     mbar_init(&bars->turn[0], 1);
     mbar_init(&bars->turn[1], 1);
-    mbar_init(&bars->kc_full, 1);
-    mbar_init(&bars->vc_full, 1);
-    for (int s = 0; s < kPfStages; ++s) mbar_init(&bars->vs_full[s], 1);
+    if (KV8) {
+      mbar_init(&bars->kc_full, 1);
+      mbar_init(&bars->vc_full, 1);
+      for (int s = 0; s < kPfStages; ++s) mbar_init(&bars->vs_full[s], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->p_full[i], 128);
       mbar_init(&bars->o_full[i], 1);
       mbar_init(&bars->o_empty[i], DIFF ? 256 : 128);  // DIFF: both warpgroups read both
-      mbar_init(&bars->xl_full[i], 128);
-      mbar_init(&bars->xs_full[i], 128);
+      if (JOIN) {
+        mbar_init(&bars->p_half[i], 128);
+        mbar_init(&bars->xl_full[i], 128);
+        mbar_init(&bars->xs_full[i], 128);
+      }
     }
     bars->abort = 0;
     fence_mbar_init();
@@ -779,15 +796,21 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       }
     };
     // O_i (+)= P_i V over the first nk 16-key steps of the block
-    // (WIN: from step k0 on, which the caller keeps below nk)
+    // (HALF: steps [k0, nk), none if empty)
     auto issue_PV = [&](int i, int st, bool acc, int nk, int k0) {
       const uint32_t d = tmem + 256 + i * D;
       const uint32_t p = tmem + i * 128;
       const uint32_t b0 = tc::opaque(st ? lV1 : lV0);
-      if (WIN && k0 > 0) {
-        for (int kk = k0; kk < nk; ++kk)
-          tc::mma_ts_lo_pred(d, p + kk * 8, b0 + (uint32_t)((kk * 2048) >> 4), idPV,
-                             acc || kk > k0 ? 1u : 0u);
+      if constexpr (HALF) {
+        if (nk - k0 == 4) {
+          const uint32_t pp = p + k0 * 8, bb = tc::opaque(b0 + k0 * 128);
+          tc::mma_ts_lo_pred(d, pp, bb, idPV, acc ? 1u : 0u);
+#pragma unroll
+          for (int kk = 1; kk < 4; ++kk) tc::mma_ts_lo<1>(d, pp + kk * 8, bb + kk * 128, idPV);
+        } else {
+          for (int kk = k0; kk < nk; ++kk)
+            tc::mma_ts_lo_pred(d, p + kk * 8, b0 + kk * 128, idPV, acc || kk > k0 ? 1u : 0u);
+        }
         return;
       }
       tc::mma_ts_lo_pred(d, p, b0, idPV, acc ? 1u : 0u);
@@ -826,12 +849,14 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         // matter.  Tile 0's issuer zeroes before its PV; tile 1's issues its PV only after
         // tile 0's turn, which ends after the zeroing.
         int nk = KB / 16, k0 = 0;
+        bool zeroes = false;  // tile 0's issuer zeroes rows of this block's V
         const int nvalid = w.max_kv - ((WIN ? w.kb0 : 0) + kb) * KB;
         if (WIN && kb == 0 && w.lo_off > 0) {
           // the tile's first visible key: the product starts at its 16-key step, and that
           // step's rows before it are zeroed (they may hold anything)
           k0 = w.lo_off / 16;
-          if (qi == 0 && w.lo_off % 16) {
+          zeroes = w.lo_off % 16 != 0;
+          if (qi == 0 && zeroes) {
             for (int hf = 0; hf < Cfg::kHalves; ++hf) {
               uint4 *base = reinterpret_cast<uint4 *>(smem + Cfg::kV + st * Cfg::kTile +
                                                       hf * kBoxBytes + k0 * 16 * 128);
@@ -843,6 +868,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         if (kb + 1 == w.nkb && nvalid < KB) {
           nk = (nvalid + 15) / 16;
           const int n16 = (nk * 16 - nvalid) * 8;
+          zeroes |= n16 > 0;
           if (!KV8 && qi == 0 && n16 > 0) {  // FP8 pages: cleared when widened
             for (int hf = 0; hf < Cfg::kHalves; ++hf) {
               uint4 *base = reinterpret_cast<uint4 *>(smem + Cfg::kV + st * Cfg::kTile +
@@ -852,19 +878,30 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
             fence_proxy_async();
           }
         }
-        if (!pf_wait(&bars->p_full[qi], (sc + kk) & 1u, err, abort)) { ok = false; break; }
-        if (kk == 0 && nitem > 0 && !pf_wait(&bars->o_empty[qi], (nitem - 1) & 1, err, abort)) {
-          ok = false;
-          break;
-        }
         // every wait of the block comes before its MMAs, so that PV_i(kb) and S_i(kb+1)
         // go to the tensor pipe as one burst of 16 (a wait between them would leave the
-        // pipe idle: each costs ~100 cycles even when the phase has completed)
+        // pipe idle: each costs ~100-300 cycles even when the phase has completed), and P's,
+        // which comes last, is the last of them
         const uint32_t nxt = cur + 1;
         const int st2 = nxt % kPfStages;
         if (!last && !pf_wait(&bars->k_full[st2], (nxt / kPfStages) & 1u, err, abort)) {
           ok = false;
           break;
+        }
+        if (kk == 0 && nitem > 0 && !pf_wait(&bars->o_empty[qi], (nitem - 1) & 1, err, abort)) {
+          ok = false;
+          break;
+        }
+        int k_done = k0;
+        if (HALF) {
+          // the products of the block's first 64 keys, out of turn (tile 1's only where it need
+          // not wait for the rows that tile 0's side zeroes)
+          if (!pf_wait(&bars->p_half[qi], (sc + kk) & 1u, err, abort)) { ok = false; break; }
+          if (k0 < min(nk, 4) && (qi == 0 || !zeroes)) {
+            tc::fence_after_sync();
+            k_done = min(nk, 4);
+            issue_PV(qi, st, kk > 0, k_done, k0);
+          }
         }
         // strict alternation of the two issuers, block by block: tile 0's PV(kb), S(kb+1),
         // then tile 1's, then tile 0's PV(kb+1) ...  A thread waits for its turn while the
@@ -874,8 +911,9 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           ok = false;
           break;
         }
+        if (!pf_wait(&bars->p_full[qi], (sc + kk) & 1u, err, abort)) { ok = false; break; }
         tc::fence_after_sync();
-        issue_PV(qi, st, kk > 0, nk, k0);
+        issue_PV(qi, st, kk > 0 || k_done > k0, nk, k_done);
         if (last) tc::commit(&bars->o_full[qi]);
         tc::commit(&bars->v_empty[st]);
         if (!last) {
@@ -1019,6 +1057,18 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
             alpha = exp2_approx(m_run - m_new);
             m_run = m_new;
           }
+          auto rescale_o = [&]() {
+            if (kk == 0 || !__any_sync(0xffffffffu, need)) return;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tc::ld32(tO + c * 32, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tc::st32(tO + c * 32, o);
+            }
+          };
           // p = 2^(s * scale_log2 - m), one packed FMA per pair, then ex2; a row with no
           // valid key yet uses m = 0 so that its -inf scores give exactly 0.  P (f16) goes
           // to the first 64 columns of S (already in registers): half hh lands in columns
@@ -1051,20 +1101,17 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
               pk[j >> 1] = *reinterpret_cast<uint32_t *>(&hp);
             }
             tc::st16(tS + 16 * q4, pk);
+            if (HALF && q4 == 1) {
+              // half of P: its products may start while the other half is computed
+              rescale_o();
+              tc::wait_st();
+              tc::fence_before_sync();
+              mbar_arrive(&bars->p_half[wg]);
+            }
           }
           const float rs = rs2.x + rs2.y;
           l_run = l_run * alpha + rs;
-          if (kk > 0 && __any_sync(0xffffffffu, need)) {
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tc::ld32(tO + c * 32, o);
-              tc::wait_ld();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-              tc::st32(tO + c * 32, o);
-            }
-          }
+          if (!HALF) rescale_o();
           if (MASK && wg == 0) {
             // free cells may hold NaN: their V rows are zeroed before this block's PV
             // products (the other tile's issuer runs its PV only after tile 0's turn)
