@@ -27,6 +27,8 @@ namespace pa {
 //                                  then the page ids of that unit's key block (8 ints, -1 past its end)
 //   pf_start       int4 [C]      first prefill unit of each CTA: (tile, item in tile, kb,
 //                                  tile * items per tile + item of the CTA's last unit)
+//   pf_first       PfFirst [C]   (differential and windowed plans) where each CTA's prefill work
+//                                  begins, with what its roles would look up otherwise
 //   pf_split       int4 [C]      (differential and windowed plans) the prefill items that are
 //                                  cut over CTAs: (tile, 2 item + slot of the first part's
 //                                  record, first CTA, parts)
@@ -86,9 +88,22 @@ constexpr int kPfMinRange = 4;
 // each of four (an item has at most one part per SM).
 constexpr int kJoinScratchParts = 256, kJoinFewParts = kJoinScratchParts / 4;
 
+// One 128-byte line per CTA: a CTA's first loads are its own record, at once, instead of the
+// header, the start, the tile and the page table one after the other.
+struct PfFirst {
+  int4 seg;    // first piece: tile, item in tile, key blocks [z, w) of the item
+  int4 tl;     // its tile record (see tiles)
+  int4 run;    // its unit, the end of its run, the item's first unit, units in all
+  int4 rest;   // second run: tile (-1: none), item, key block, -
+  int4 rng;    // [w0, w1) of the CTA (x == y: no work), of the second run's end z, even cut w
+  int pages[8];  // page ids of the first piece's first key block
+  int4 pad;
+};
+static_assert(sizeof(PfFirst) == 128, "one line");
+
 struct WsLayout {
-  size_t tiles, dec_tok, tok_unit_off, flags, runs, tile_off, dec_start, pf_start, pf_split;
-  size_t pf_cnt;
+  size_t tiles, dec_tok, tok_unit_off, flags, runs, tile_off, dec_start, pf_start, pf_first;
+  size_t pf_split, pf_cnt;
   size_t dec_cnt;
   size_t partials, dec_partials, total;
   int n_cnt;  // entries of pf_cnt
@@ -111,6 +126,7 @@ __host__ __device__ inline WsLayout ws_layout(int T, int Hq, int Hkv, int D, int
   l.tile_off = o;     o = align_up(o + (Tm + 1) * 4, 256);
   l.dec_start = o;    o = align_up(o + (size_t)C * 64, 256);
   l.pf_start = o;     o = align_up(o + (size_t)C * 16, 256);
+  l.pf_first = o;     if (both) o = align_up(o + (size_t)C * sizeof(PfFirst), 256);
   l.pf_split = o;     if (both) o = align_up(o + (size_t)C * 16, 256);
   l.n_cnt = (int)(Tm * Hkv * NP * 8);
   l.pf_cnt = o;       o = align_up(o + (size_t)l.n_cnt * 4, 256);

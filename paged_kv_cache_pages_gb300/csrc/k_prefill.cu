@@ -332,10 +332,12 @@ struct PfWork {
   int4 start;           // first (tile, item, key block) of this CTA
   long long W, w0, w1;  // total work units; this CTA's range [w0, w1)
   long long cut0;       // where an even cut would start the range (w0 may lie before it)
+  const PfFirst *first;  // WHOLE: the CTA's first record
   int C;                // CTAs the plan was cut for
 };
 
-// WHOLE: a plan that keeps short items whole (differential and windowed attention).
+// WHOLE: a plan that keeps short items whole (differential and windowed attention), with a first
+// record per CTA; `start` is not set then.
 template <bool WHOLE = false>
 __device__ __forceinline__ PfWork pf_work(const AttnArgs &a, int NP, int G, int item_heads = 2) {
   uint64_t wsp = reinterpret_cast<uint64_t>(a.ws);
@@ -343,11 +345,21 @@ __device__ __forceinline__ PfWork pf_work(const AttnArgs &a, int NP, int G, int 
   const unsigned char *ws = reinterpret_cast<const unsigned char *>(wsp);
   const WsHeader *hdr = reinterpret_cast<const WsHeader *>(ws);
   PfWork r;
-  r.C = hdr->C;
-  r.W = hdr->pf_work;
   const int c = blockIdx.x;
-  r.cut0 = r.w0 = (long long)c * r.W / r.C;
-  r.w1 = (long long)(c + 1) * r.W / r.C;
+  if (WHOLE) {
+    r.first = reinterpret_cast<const PfFirst *>(ws + a.lay.pf_first) + c;
+    const int4 g = r.first->rng;
+    r.w0 = g.x;
+    r.w1 = g.y;
+    r.cut0 = g.w;
+    r.C = 0;
+    r.W = 0;
+  } else {
+    r.C = hdr->C;
+    r.W = hdr->pf_work;
+    r.cut0 = r.w0 = (long long)c * r.W / r.C;
+    r.w1 = (long long)(c + 1) * r.W / r.C;
+  }
   r.sx.tiles = reinterpret_cast<const int4 *>(ws + a.lay.tiles);
   r.sx.tile_off = reinterpret_cast<const int *>(ws + a.lay.tile_off);
   r.sx.Hkv = a.Hkv;
@@ -355,19 +367,32 @@ __device__ __forceinline__ PfWork pf_work(const AttnArgs &a, int NP, int G, int 
   r.sx.G = G;
   r.sx.item_heads = item_heads;
   r.sx.items_per_tile = a.Hkv * NP;
-  r.start = reinterpret_cast<const int4 *>(ws + a.lay.pf_start)[c];
-  if (WHOLE) {
-    // the planner moved cuts in short items back to the items' starts
-    auto unit_of = [&](int4 p) {
-      return (long long)r.sx.tile_off[p.x] + (long long)p.y * pf_item_units(r.sx.tiles[p.x].z) +
-             p.z;
-    };
-    r.w0 = r.W > 0 ? unit_of(r.start) : 0;
-    r.w1 = c + 1 == r.C || r.W == 0
-               ? r.W
-               : unit_of(reinterpret_cast<const int4 *>(ws + a.lay.pf_start)[c + 1]);
-  }
+  if (!WHOLE) r.start = reinterpret_cast<const int4 *>(ws + a.lay.pf_start)[c];
   return r;
+}
+
+// The same, read from the CTA's record.
+__device__ __forceinline__ bool seg_first_rec(Seg &s, const SegCtx &x, const PfWork &pw) {
+  if (pw.w0 >= pw.w1) return false;
+  const int4 a = pw.first->seg, tl = pw.first->tl, run = pw.first->run;
+  s.rest = pw.first->rest;
+  s.tile = a.x;
+  s.j = a.y;
+  s.kb_b = a.z;
+  s.kb_e = a.w;
+  s.tile_start = tl.x;
+  s.n_tok = tl.y & 0xffff;
+  s.lo_off = tl.y >> 16;
+  s.nkb = tl.z;
+  s.max_kv = tl.w;
+  s.kb0 = (s.max_kv + KB - 1) / KB - s.nkb;
+  seg_heads(s, x);
+  s.w = run.x;
+  s.w_end = run.y;
+  s.item_start = run.z;
+  s.rest_w0 = pw.w0;
+  s.rest_w1 = pw.first->rng.z;
+  return true;
 }
 
 // First piece of the CTA's work (see Seg for the order of its two runs).
@@ -587,10 +612,15 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   const int NQ = DIFF || G >= 2 ? 2 : 1;            // query tiles of an item
   const int NP = DIFF ? G : G >= 2 ? G / 2 : 1;     // items per tile and KV head
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto first_piece = [](Seg &s, const SegCtx &x, const PfWork &pw) {
+    return JOIN ? seg_first_rec(s, x, pw) : seg_first(s, x, pw);
+  };
   const int C = hdr->C;
   const int c = blockIdx.x;
   // the split-KV launch behind this one may take the SMs that this grid leaves
   if (JOIN) asm volatile("griddepcontrol.launch_dependents;");
+  int4 rng = make_int4(0, 0, 0, 0);  // JOIN: the CTA's unit range, loaded beside the header
+  if (JOIN) rng = reinterpret_cast<const PfFirst *>(a.ws + a.lay.pf_first)[c].rng;
   if (c >= C) return;
   if (hdr->kind != plan_kind(NP, WIN)) {  // the tile records are another operator's
     if (c == 0 && tid == 0) atomicOr(err, PA_ERR_PLAN);
@@ -598,13 +628,21 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   }
   const int window = WIN ? hdr->window : 0;
   // tiles whose tokens all have kv_len 0 own no work unit: their rows are zero
-  for (int t = c; t < hdr->n_tiles; t += C) {
-    const int4 tl = tiles[t];
-    if (tl.z != 0) continue;
-    for (int x = tid; x < (tl.y & 0xffff) * a.Hq * (D / 8); x += blockDim.x)
-      reinterpret_cast<uint4 *>(a.out + (size_t)tl.x * a.Hq * D)[x] = make_uint4(0, 0, 0, 0);
-  }
-  {
+  auto zero_rows = [&](int x0, int step) {
+    for (int t = c; t < hdr->n_tiles; t += C) {
+      const int4 tl = tiles[t];
+      if (tl.z != 0) continue;
+      for (int x = x0; x < (tl.y & 0xffff) * a.Hq * (D / 8); x += step)
+        reinterpret_cast<uint4 *>(a.out + (size_t)tl.x * a.Hq * D)[x] = make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (JOIN) {  // a CTA with work leaves them to its idle warp
+    if (rng.x >= rng.y) {
+      zero_rows(tid, blockDim.x);
+      return;
+    }
+  } else {
+    zero_rows(tid, blockDim.x);
     const PfWork pw = pf_work<JOIN>(a, NP, G, kItemHeads);
     if (pw.w0 >= pw.w1) return;
   }
@@ -697,7 +735,10 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         const bool mine = box_j >= j0 && box_j < npg;
         int y = oob_row;
         if (mine) {
-          const int page = row[((WIN ? w.kb0 : 0) + kb) * pages_per_block + box_j];
+          // (the first block's page ids come with the CTA's record)
+          const int page = JOIN && it == 0
+                               ? pw.first->pages[box_j]
+                               : row[((WIN ? w.kb0 : 0) + kb) * pages_per_block + box_j];
           if (page < 0 || page >= a.num_pages) atomicOr(err, PA_ERR_PAGE_RANGE);
           else y = (page * a.Hkv + w.g) * a.P;
         }
@@ -713,7 +754,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         ++it;
         return true;
       };
-      for (bool more = seg_first(w, sx, pw); more; more = seg_next(w, sx)) {
+      for (bool more = first_piece(w, sx, pw); more; more = seg_next(w, sx)) {
         row = a.tpt + (size_t)w.tile_start * a.max_pages;
         int kb = w.kb_b;
         const int qb = nitem % Cfg::kQBufs;
@@ -749,6 +790,8 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         ++nitem;
       }
     }
+   } else if (JOIN && warp == kWarpTma + 3) {
+    zero_rows(lane, 32);
    } else if ((warp == kWarpMma || warp == kWarpMma + 1) && lane == 0 &&
               warp - kWarpMma < NQ) {
     // ------------------------------------------------------------ MMA issuers
@@ -825,7 +868,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
     uint32_t it = 0, sc = 0;
     int nitem = 0;
     Seg w;
-    for (bool more = seg_first(w, sx, pw); more; more = seg_next(w, sx)) {
+    for (bool more = first_piece(w, sx, pw); more; more = seg_next(w, sx)) {
       const int nseg = w.kb_e - w.kb_b;
       const int qb = nitem % Cfg::kQBufs;
       bool ok = pf_wait(&bars->q_full[qb], (nitem / Cfg::kQBufs) & 1, err, abort);
@@ -950,7 +993,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       int *cnt = reinterpret_cast<int *>(a.ws + a.lay.pf_cnt);
       Seg w;
       int l_tile = -1, L = 0;  // the row's kv_len, loaded once per tile
-      for (bool more = seg_first(w, sx, pw); more; more = seg_next(w, sx)) {
+      for (bool more = first_piece(w, sx, pw); more; more = seg_next(w, sx)) {
         const int h = !DIFF && wg ? w.h1 : w.h0;
         const int tok = w.tile_start + row;
         const bool valid = row < w.n_tok;

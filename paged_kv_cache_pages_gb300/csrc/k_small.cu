@@ -433,8 +433,31 @@ k_plan(const int32_t *__restrict__ tpt, int max_pages, const int32_t *__restrict
       const int nkl = tiles[tl].z;
       const int jl = nkl > 0 ? (int)((wl - tile_off[tl]) / pf_item_units(nkl)) : 0;
       pf_start[c] = make_int4(p0.x, p0.y, p0.z, tl * Hkv * NP + jl);
+      if (whole_items) {
+        // as seg_first places it: the run of the item that holds the last unit first
+        PfFirst f;
+        const long long wi = unit_of(make_int3(tl, jl, 0));
+        const bool two = wi > w && wi < we;
+        const int3 s = two ? make_int3(tl, jl, 0) : p0;
+        f.tl = tiles[s.x];
+        const int istart = (int)unit_of(make_int3(s.x, s.y, 0));
+        const int w_first = two ? (int)wi : (int)w;
+        f.seg = make_int4(s.x, s.y, w_first - istart, min(f.tl.z, (int)we - istart));
+        f.run = make_int4(w_first, (int)we, istart, (int)W);
+        f.rest = two ? make_int4(p0.x, p0.y, p0.z, 0) : make_int4(-1, 0, 0, 0);
+        f.rng = make_int4((int)w, (int)we, (int)wi, (int)((long long)c * W / Cp));
+        const int kb = (f.tl.w + KB - 1) / KB - f.tl.z + f.seg.z;  // from the row's start
+        const int npg = w < we ? (min(KB, f.tl.w - kb * KB) + P - 1) / P : 0;
+        const int32_t *row = tpt + (size_t)f.tl.x * max_pages + (size_t)kb * (KB / P);
+        for (int j = 0; j < 8; ++j) f.pages[j] = j < npg ? row[j] : -1;
+        f.pad = make_int4(0, 0, 0, 0);
+        reinterpret_cast<PfFirst *>(ws + lay.pf_first)[c] = f;
+      }
     }
   }
+  if (whole_items && W <= 0)
+    for (int c = tid; c < Cp; c += kPlanThreads)
+      reinterpret_cast<PfFirst *>(ws + lay.pf_first)[c].rng = make_int4(0, 0, 0, 0);
   // 7. the items that the prefill's cuts divide, at the first cut of each
   if (whole_items) {
     __syncthreads();
