@@ -28,6 +28,14 @@
   python -m paged_kv_cache_pages_gb300.profile_case copy [--reps R]
       page copy of copy-on-write forks: 512 of 1280 pages (8 KV heads x 128 rows
       x d 128, K and V) copied to 512 others per call.
+  python -m paged_kv_cache_pages_gb300.profile_case diff|window [--reps R] [--pools N]
+      differential attention, or a window of 1024 with sinks, on the decode layer's
+      tokens, N pool copies in turn.
+  python -m paged_kv_cache_pages_gb300.profile_case diff_prefill|window_prefill [--ubatch U]
+      the same on a prefill ubatch (window 4096).
+  python -m paged_kv_cache_pages_gb300.profile_case batch [--reps R]
+      a step's tables from request lengths: 512 decoding requests, 40 that finished,
+      64 chunks of 200, pages of 16 positions, a pool of 280,000 pages.
 
 Prints the average time of the call (CUDA events) and exits 0.
 """
@@ -223,10 +231,100 @@ def copy(reps: int):
     print(f"copy_pages: {ms * 1e3:.1f} us/call {nbytes / ms / 1e6:.1f} GB/s (read + written)")
 
 
+def _other(kind, q, tpt, kv, scale, Hkv, P, window):
+    """(plan, run) of the differential or the windowed attention: run(k_pages, v_pages)."""
+    T, Hq, d = q.shape
+    out, g = torch.empty_like(q), torch.Generator(device="cuda").manual_seed(3)
+    if kind == "diff":
+        ws = pa.new_diff_workspace(T, Hq, Hkv, d)
+        lam = torch.rand(Hq, generator=g, device="cuda")
+        w = torch.ones(d, device="cuda")
+        pa.plan_diff(tpt, kv, Hq, Hkv, P, d, ws)
+        return ws, lambda k, v: pa.diff_run(q, k, v, tpt, kv, scale * 2 ** 0.5, lam, w, out=out,
+                                            workspace=ws)
+    ws = pa.new_workspace(T, Hq, Hkv, d)
+    sink = torch.randn(Hq, generator=g, device="cuda")
+    pa.plan_window(tpt, kv, Hq, Hkv, P, d, window, ws)
+    return ws, lambda k, v: pa.window_run(q, k, v, tpt, kv, scale, sink, out=out, workspace=ws)
+
+
+def other_decode(kind: str, reps: int, n_pools: int):
+    c = workloads.decode(0)
+    dev = "cuda"
+    tpt, kv, slot = pa.expand_ubatch(
+        torch.from_numpy(c.seq_page_table()).to(dev), torch.from_numpy(c.tok_seq).to(dev),
+        torch.from_numpy(c.tok_pos).to(dev), c.P)
+    kp, vp = (torch.from_numpy(x.view(np.float16)).to(dev) for x in (c.k_pool, c.v_pool))
+    pa.kv_append(torch.from_numpy(c.k_new.view(np.float16)).to(dev),
+                 torch.from_numpy(c.v_new.view(np.float16)).to(dev), slot, kp, vp)
+    pools = [(kp, vp)] + [(kp.clone(), vp.clone()) for _ in range(n_pools - 1)]
+    q = torch.from_numpy(c.q.view(np.float16)).to(dev)
+    ws, run = _other(kind, q, tpt, kv, c.scale, c.Hkv, c.P, 1024)
+    turn = [0]
+
+    def fn():
+        turn[0] += 1
+        run(*pools[turn[0] % len(pools)])
+
+    ms = _time(fn, reps)
+    if pa.read_error(ws):
+        raise SystemExit("device error word set")
+    keys = np.minimum(c.seq_len, 1024) if kind == "window" else c.seq_len
+    nbytes = float(keys.astype(np.int64).sum()) * c.Hkv * c.d * 4
+    print(f"{kind} {c.name}: {ms * 1e3:.1f} us/call {nbytes / ms / 1e6:.1f} GB/s "
+          f"({len(pools)} pools in turn, eager launches)")
+
+
+def other_prefill(kind: str, ubatch: int, reps: int):
+    wl = workloads.Prefill8x16K(0)
+    dev = "cuda"
+    kp, vp = (torch.from_numpy(x.view(np.float16)).to(dev) for x in wl.pool_final())
+    ts, tp, q, _, _ = wl.ubatch(ubatch)
+    q_d = torch.from_numpy(q.view(np.float16)).to(dev)
+    tpt, kv, _ = pa.expand_ubatch(torch.from_numpy(wl.seq_page_table).to(dev),
+                                  torch.from_numpy(ts).to(dev), torch.from_numpy(tp).to(dev), wl.P)
+    ws, run = _other(kind, q_d, tpt, kv, wl.scale, wl.Hkv, wl.P, 4096)
+    ms = _time(lambda: run(kp, vp), reps)
+    if pa.read_error(ws):
+        raise SystemExit("device error word set")
+    keys = tp.astype(np.int64) + 1
+    flops = 4.0 * wl.d * wl.Hq * float((np.minimum(keys, 4096) if kind == "window" else keys).sum())
+    print(f"{kind} prefill ubatch {ubatch}: T={ts.shape[0]} {ms * 1e3:.1f} us/call "
+          f"{flops / ms / 1e9:.1f} TFLOP/s")
+
+
+def batch(reps: int):
+    dev, P, max_pages, N = "cuda", 16, 2048, 280_000
+    rng = np.random.default_rng(7100)
+    length = rng.integers(1, 12_000, 616).astype(np.int32)
+    new = np.r_[np.ones(512), np.full(64, 200), np.full(40, -1)].astype(np.int32)
+    npg = -(-length // P)
+    while npg.sum() > N * 3 // 4:
+        length //= 2
+        npg = -(-length // P)
+    perm, table, ref = rng.permutation(N), np.full((616, max_pages), -1, np.int32), np.zeros(N, np.int32)
+    for i, at in enumerate(np.cumsum(npg) - npg):
+        table[i, :npg[i]] = perm[at:at + npg[i]]
+    ref[perm[:npg.sum()]] = 1
+    t0, r0, ln, nw = (torch.from_numpy(x).to(dev) for x in (table, ref, length, new))
+    T = int(np.maximum(new, 0).sum())
+    t, r, out = t0.clone(), r0.clone(), pa.new_batch(616, max_pages, T)
+
+    def fn():
+        t.copy_(t0)
+        r.copy_(r0)
+        pa.batch_build(t, ln, nw, r, P, T, out=out)
+
+    ms = _time(fn, reps)
+    print(f"batch: {ms * 1e3:.1f} us/call with the copies that restore the pool; T={T}, "
+          f"{4e-6 * T * max_pages:.0f} MB of token rows")
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("case", choices=["prefill", "prefill_fp8", "decode", "longtail", "copy",
-                                     "span", "fp8", "fp8_longtail"])
+                                     "span", "fp8", "fp8_longtail", "diff", "window",
+                                     "diff_prefill", "window_prefill", "batch"])
     ap.add_argument("--ubatch", type=int, default=48)
     ap.add_argument("--reps", type=int, default=3)
     ap.add_argument("--pools", type=int, default=8)
@@ -245,6 +343,12 @@ def main():
         fp8(a.reps, a.pools)
     elif a.case == "fp8_longtail":
         fp8(a.reps, a.pools, longtail=True)
+    elif a.case in ("diff", "window"):
+        other_decode(a.case, a.reps, a.pools)
+    elif a.case in ("diff_prefill", "window_prefill"):
+        other_prefill(a.case.split("_")[0], a.ubatch, a.reps)
+    elif a.case == "batch":
+        batch(a.reps)
     else:
         copy(a.reps)
 
