@@ -28,7 +28,8 @@
 // The softmax warpgroups raise their register budget with setmaxnreg so that a
 // softmax thread holds its whole 128-column score row in registers (one TMEM round
 // trip per block); the third warpgroup lowers its own.
-// TMEM (512 columns): S0 | S1 | O0 | O1.  P_i (f16) overwrites the first 64
+// TMEM (512 columns): S0 | S1 | O0 | O1 (d 64: O is 64 columns wide, and the differential and
+// windowed kinds keep P0 | P1 behind it).  P_i (f16) overwrites the first 64
 // columns of S_i.  Tile i's issuer runs PV_i(kb) then S_i(kb+1) (in order on the
 // tensor core, so S_i(kb+1) overwrites P_i only after PV_i read it); the softmax of
 // one tile runs while the tensor core works on the other.
@@ -95,8 +96,10 @@ struct PfBars {
       uint64_t vs_full[kPfStages];
     };
     struct {
-      // WIN: P of the block's first 64 keys is in TMEM
+      // HALF: P of the block's first 64 keys is in TMEM; SPLIT: the products have read P
       uint64_t p_half[2];
+      // SPLIT: the softmax has read S
+      uint64_t s_read[2];
       // DIFF: a warpgroup's row sums, then its sums of squares, are in shared memory
       uint64_t xl_full[2], xs_full[2];
     };
@@ -590,10 +593,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   constexpr bool MASK = VAR == kPfMask, KV8 = VAR == kPfKv8;
   constexpr bool DIFF = VAR == kPfDiff, WIN = VAR == kPfWin;
-  // The products of a block's first 64 keys start while the softmax computes the other half of
-  // P.  Measured: windowed chunks 138 to 127 us; differential ones, whose blocks have fewer MMAs
-  // to hide behind the second hand-off, 413 to 421 us, so they keep one.
-  constexpr bool HALF = WIN;
+  // How a block's products overlap its softmax.  SPLIT (d 64, whose accumulators leave 128 TMEM
+  // columns): P has columns of its own, so that S of the next block is computed while the softmax
+  // works on this one; four 512-token chunks 361 to 340 us (differential), 207 to 192 us
+  // (windowed), nothing lost at short ones.  HALF: the products of a block's first 64 keys start
+  // while the softmax computes the other half of P; windowed chunks at d 128 138 to 127 us, but
+  // differential ones, whose blocks have fewer MMAs to hide behind the second hand-off, 413 to
+  // 421 us, so they keep one.
+  constexpr bool SPLIT = (DIFF || WIN) && D == 64;
+  constexpr bool HALF = WIN && !SPLIT;
   constexpr bool JOIN = DIFF || WIN;  // split items are joined by the split-KV launch (join.cuh)
   constexpr int kItemHeads = DIFF ? 1 : 2;
   static_assert(!KV8 || D == 128, "FP8 pages: d 128");
@@ -671,7 +679,8 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       mbar_init(&bars->o_full[i], 1);
       mbar_init(&bars->o_empty[i], DIFF ? 256 : 128);  // DIFF: both warpgroups read both
       if (JOIN) {
-        mbar_init(&bars->p_half[i], 128);
+        mbar_init(&bars->p_half[i], SPLIT ? 1 : 128);
+        mbar_init(&bars->s_read[i], 128);
         mbar_init(&bars->xl_full[i], 128);
         mbar_init(&bars->xs_full[i], 128);
       }
@@ -842,10 +851,14 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
     // (HALF: steps [k0, nk), none if empty)
     auto issue_PV = [&](int i, int st, bool acc, int nk, int k0) {
       const uint32_t d = tmem + 256 + i * D;
-      const uint32_t p = tmem + i * 128;
+      const uint32_t p = SPLIT ? tmem + 384 + i * 64 : tmem + i * 128;
       const uint32_t b0 = tc::opaque(st ? lV1 : lV0);
-      if constexpr (HALF) {
-        if (nk - k0 == 4) {
+      if constexpr (HALF || (SPLIT && WIN)) {
+        if (SPLIT && nk - k0 == 8) {
+          tc::mma_ts_lo_pred(d, p, b0, idPV, acc ? 1u : 0u);
+#pragma unroll
+          for (int kk = 1; kk < 8; ++kk) tc::mma_ts_lo<1>(d, p + kk * 8, b0 + kk * 128, idPV);
+        } else if (nk - k0 == 4) {
           const uint32_t pp = p + k0 * 8, bb = tc::opaque(b0 + k0 * 128);
           tc::mma_ts_lo_pred(d, pp, bb, idPV, acc ? 1u : 0u);
 #pragma unroll
@@ -874,6 +887,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       bool ok = pf_wait(&bars->q_full[qb], (nitem / Cfg::kQBufs) & 1, err, abort);
       const int st0 = it % kPfStages;
       ok = ok && pf_wait(&bars->k_full[st0], (it / kPfStages) & 1u, err, abort);
+      if (SPLIT && it > 0) ok = ok && pf_wait(&bars->s_read[qi], (it - 1) & 1u, err, abort);
       if (!ok) break;
       tc::fence_after_sync();
       issue_S(qi, st0, qb);
@@ -884,6 +898,19 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         const uint32_t cur = it + kk;
         const int st = cur % kPfStages;
         const bool last = kk + 1 == nseg;
+        if (SPLIT && !last) {
+          // S(kb + 1) as soon as the softmax has read S(kb): it is done before P(kb) is
+          const int st2 = (cur + 1) % kPfStages;
+          if (!pf_wait(&bars->k_full[st2], ((cur + 1) / kPfStages) & 1u, err, abort) ||
+              !pf_wait(&bars->s_read[qi], cur & 1u, err, abort)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          issue_S(qi, st2, qb);
+          tc::commit(&bars->s_full[qi]);
+          tc::commit(&bars->k_empty[st2]);
+        }
         if (!pf_wait(&bars->v_full[st], (cur / kPfStages) & 1u, err, abort)) { ok = false; break; }
         // the item's last block may hold fewer than 128 valid keys: the PV product then
         // runs only over the 16-key steps that hold valid keys, and the rows of the last
@@ -927,7 +954,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         // which comes last, is the last of them
         const uint32_t nxt = cur + 1;
         const int st2 = nxt % kPfStages;
-        if (!last && !pf_wait(&bars->k_full[st2], (nxt / kPfStages) & 1u, err, abort)) {
+        if (!SPLIT && !last && !pf_wait(&bars->k_full[st2], (nxt / kPfStages) & 1u, err, abort)) {
           ok = false;
           break;
         }
@@ -949,16 +976,23 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         // strict alternation of the two issuers, block by block: tile 0's PV(kb), S(kb+1),
         // then tile 1's, then tile 0's PV(kb+1) ...  A thread waits for its turn while the
         // other's MMAs run, and the two softmax warpgroups stay half a period apart.
+        // (SPLIT: no alternation of the bursts: tile 1's products follow tile 0's zeroing, and
+        // tile 0 stays at most a block ahead, so that no phase of a turn passes unseen.)
         if (NQ == 2 && (qi == 1 || cur > 0) &&
             !pf_wait(&bars->turn[qi], (qi ? cur : cur - 1) & 1u, err, abort)) {
           ok = false;
           break;
         }
+        if (SPLIT && NQ == 2) mbar_arrive(&bars->turn[qi ^ 1]);
         if (!pf_wait(&bars->p_full[qi], (sc + kk) & 1u, err, abort)) { ok = false; break; }
         tc::fence_after_sync();
         issue_PV(qi, st, kk > 0 || k_done > k0, nk, k_done);
         if (last) tc::commit(&bars->o_full[qi]);
         tc::commit(&bars->v_empty[st]);
+        if (SPLIT) {
+          tc::commit(&bars->p_half[qi]);
+          continue;
+        }
         if (!last) {
           issue_S(qi, st2, qb);
           tc::commit(&bars->s_full[qi]);
@@ -982,6 +1016,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
     const uint32_t lane_off = (uint32_t)(wl * 32) << 16;
     const uint32_t tS = tmem + wg * 128 + lane_off;
     const uint32_t tO = tmem + 256 + wg * D + lane_off;
+    const uint32_t tP = SPLIT ? tmem + 384 + wg * 64 + lane_off : tS;
     if (wg < NQ) {
       const PfWork pw = pf_work<JOIN>(a, NP, G, kItemHeads);
       const SegCtx &sx = pw.sx;
@@ -1059,6 +1094,10 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           tc::ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(t + 64));
           tc::ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(t + 96));
           tc::wait_ld();
+          if (SPLIT) {
+            tc::fence_before_sync();
+            mbar_arrive(&bars->s_read[wg]);
+          }
           if (MASK) {
             // the kept keys as a 128-bit mask first (a rolled loop over the cells keeps
             // few registers live beside the score row), then applied to the scores
@@ -1099,6 +1138,10 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           if (need) {
             alpha = exp2_approx(m_run - m_new);
             m_run = m_new;
+          }
+          if (SPLIT && sc + kk > 0) {  // the products of the block before have read P and added to O
+            if (!pf_wait(&bars->p_half[wg], (sc + kk - 1) & 1u, err, abort)) { ok = false; break; }
+            tc::fence_after_sync();
           }
           auto rescale_o = [&]() {
             if (kk == 0 || !__any_sync(0xffffffffu, need)) return;
@@ -1143,7 +1186,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
               __half2 hp = __floats2half2_rn(p.x, p.y);
               pk[j >> 1] = *reinterpret_cast<uint32_t *>(&hp);
             }
-            tc::st16(tS + 16 * q4, pk);
+            tc::st16(tP + 16 * q4, pk);
             if (HALF && q4 == 1) {
               // half of P: its products may start while the other half is computed
               rescale_o();
