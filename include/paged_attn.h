@@ -90,7 +90,7 @@ extern "C" {
                                    batch build: a request's lengths do not fit its row */
 #define PA_ERR_NO_SPACE 0x20    /* batch build: requests left out (free pages or tokens ran out) */
 #define PA_ERR_REFCOUNT 0x40    /* batch build: a finished row names a page that is free */
-#define PA_ERR_PLAN 0x80        /* the workspace holds the plan of another operator */
+#define PA_ERR_PLAN 0x80        /* the workspace holds a plan of another operator or other sizes */
 
 /* Human-readable text of a status code (static storage). */
 const char *paged_attn_strerror(int status);
@@ -153,7 +153,8 @@ int paged_expand_ubatch(const int32_t *seq_page_table, int n_seq, int max_pages,
  *   4. an admitted request's new pages (those of its positions past ceil(seq_len / P) * P)
  *      are taken with reference count 1 and written behind its last entry.
  * A request must own its last, partly filled page (pa_pool_fork).  The arrays must not
- * overlap, but for seq_len_out.  n_seq <= 8192 (else PA_EUNSUPPORTED).  Two launches.
+ * overlap, but for seq_len_out, and calls on one pool must follow one another (on one stream).
+ * n_seq <= 8192 (else PA_EUNSUPPORTED).  Two launches.
  */
 int paged_batch_build(int32_t *seq_page_table, int n_seq, int max_pages, const int32_t *seq_len,
                       const int32_t *new_len, int32_t *page_ref, int num_pages, int P, int T,
@@ -455,8 +456,10 @@ int paged_attn_forward_fp8(const uint16_t *q, const uint8_t *k8_pages, const uin
  * A plan of this operator has its own layout: make the workspace
  * paged_attn_diff_workspace_size bytes long and plan with paged_attn_plan_diff (arguments as
  * paged_attn_plan; one plan serves every layer).  paged_attn_diff_run runs on that plan; on
- * another operator's it sets PA_ERR_PLAN and writes nothing.  paged_attn_diff_forward is
- * the plan followed by the run.
+ * one of another operator or of other sizes it sets PA_ERR_PLAN and writes nothing.
+ * paged_attn_diff_forward is the plan followed by the run.  Runs in one workspace must follow one
+ * another (on one stream); a workspace each lets them overlap.  Two launches a run, one for a
+ * ubatch shorter than every paged_attn_set_prefill_min_run value so far (16 at first).
  */
 size_t paged_attn_diff_workspace_size(int T, int Hq, int Hkv, int d);
 int paged_attn_plan_diff(const int32_t *tok_page_table, int max_pages, const int32_t *tok_kv_len,
@@ -495,10 +498,10 @@ int paged_attn_diff_forward(const uint16_t *q, const uint16_t *k_pages, const ui
  *
  * paged_attn_plan_window plans with a window (in a workspace of
  * paged_attn_window_workspace_size bytes; one plan serves every layer with that window);
- * paged_attn_window_run runs on it, with the
- * plan's window, and on another plan sets PA_ERR_PLAN and writes nothing.  The plain run and
- * its prefill refuse a windowed plan in the same way.  paged_attn_window_forward is the plan
- * followed by the run.
+ * paged_attn_window_run runs on it, with the plan's window; on a plan of another operator or of
+ * other sizes it sets PA_ERR_PLAN and writes nothing.  (paged_attn_run and paged_attn_prefill
+ * set PA_ERR_PLAN on a windowed or differential plan; do not give them one.)
+ * paged_attn_window_forward is the plan followed by the run.
  */
 size_t paged_attn_window_workspace_size(int T, int Hq, int Hkv, int d);
 int paged_attn_plan_window(const int32_t *tok_page_table, int max_pages,

@@ -557,6 +557,8 @@ def _attn_on(fn_name, q, k_pages, v_pages, tok_page_table, tok_kv_len, scale, ex
 
 def _diff(fn_name, q, k_pages, v_pages, tok_page_table, tok_kv_len, scale, lam, norm_weight, eps,
           out_scale, out, workspace, stream):
+    if lam is None:
+        raise ValueError("lam (the weight of each head's second map) is required")
     return _attn_on(
         fn_name, q, k_pages, v_pages, tok_page_table, tok_kv_len, scale,
         (lam.data_ptr(), None if norm_weight is None else norm_weight.data_ptr(), eps, out_scale),

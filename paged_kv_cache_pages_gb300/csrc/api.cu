@@ -132,7 +132,7 @@ const char *paged_attn_strerror(int status) {
   }
 }
 
-int paged_attn_version(void) { return 100; }
+int paged_attn_version(void) { return 101; }
 
 int paged_expand_ubatch(const int32_t *seq_page_table, int n_seq, int max_pages,
                         const int32_t *tok_seq, const int32_t *tok_pos, int T, int P,
@@ -158,7 +158,8 @@ int paged_batch_build(int32_t *seq_page_table, int n_seq, int max_pages, const i
                       int *err, void *stream) {
   NvtxRange nvtx_range("paged_batch_build");
   if (n_seq < 0 || max_pages <= 0 || num_pages < 0 || P <= 0 || T < 0) return PA_EINVAL;
-  if (n_seq > kBatchMaxSeq || (int64_t)max_pages * P > INT_MAX / 2 || T > INT_MAX / 2)
+  if (n_seq > kBatchMaxSeq || (int64_t)max_pages * P > INT_MAX / 2 || T > INT_MAX / 2 ||
+      num_pages > INT_MAX / 2)
     return PA_EUNSUPPORTED;
   if (!q_start) return PA_EINVAL;
   if (n_seq > 0 && (!seq_page_table || !seq_len || !new_len || !seq_len_out)) return PA_EINVAL;

@@ -2,6 +2,7 @@
 // Inline PTX for mbarriers, bulk/tensor async copies and bounded waits.
 #pragma once
 
+#include <cstddef>
 #include <cstdint>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -60,11 +61,23 @@ struct WsHeader {
   int pad[49];
 };
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
+static_assert(offsetof(WsHeader, pf_work) == 16 && offsetof(WsHeader, kind) == 28 &&
+                  offsetof(WsHeader, Hkv) == 32 && offsetof(WsHeader, max_pages) == 44,
+              "plan_matches reads two 16-byte words");
 
 // A plan depends on the work items per tile and KV head (np) and on the window: the two
 // are checked before a kernel follows the plan's tile records.
 __host__ __device__ inline int plan_kind(int np, bool windowed) {
   return np | (windowed ? 1 << 16 : 0);
+}
+
+// Whether the workspace holds a plan of this kind for these sizes (the differential and windowed
+// kinds; the layout of the workspace and every index in the plan depend on them).
+__device__ __forceinline__ bool plan_matches(const WsHeader *hdr, int kind, int T, int Hkv, int P,
+                                             int max_pages) {
+  const int4 a = __ldcg(reinterpret_cast<const int4 *>(hdr) + 1);  // pf_work, C, T, kind
+  const int4 b = __ldcg(reinterpret_cast<const int4 *>(hdr) + 2);  // Hkv, window, P, max_pages
+  return a.w == kind && a.z == T && b.x == Hkv && b.z == P && b.w == max_pages;
 }
 
 constexpr int KB = 128;  // keys per block (decode unit and prefill key tile)

@@ -531,7 +531,7 @@ k_decode(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   if (DIFF || WIN) {
     // the plan must be of this kind (its units and the workspace layout depend on it)
     const int want = DIFF ? plan_kind(G, false) : plan_kind(G >= 2 ? G / 2 : 1, true);
-    if (__ldcg(&hdr->kind) != want) {
+    if (!plan_matches(hdr, want, a.T, a.Hkv, a.P, a.max_pages)) {
       if (tid == 0 && blockIdx.x == 0) atomicOr(&hdr->err, PA_ERR_PLAN);
       if (late) asm volatile("griddepcontrol.wait;" ::: "memory");
       return;

@@ -629,11 +629,14 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   if (JOIN) asm volatile("griddepcontrol.launch_dependents;");
   int4 rng = make_int4(0, 0, 0, 0);  // JOIN: the CTA's unit range, loaded beside the header
   if (JOIN) rng = reinterpret_cast<const PfFirst *>(a.ws + a.lay.pf_first)[c].rng;
-  if (c >= C) return;
-  if (hdr->kind != plan_kind(NP, WIN)) {  // the tile records are another operator's
+  if (!JOIN && c >= C) return;
+  // the tile records must be this operator's
+  if (JOIN ? !plan_matches(hdr, plan_kind(NP, WIN), a.T, a.Hkv, a.P, a.max_pages)
+           : hdr->kind != plan_kind(NP, false)) {
     if (c == 0 && tid == 0) atomicOr(err, PA_ERR_PLAN);
     return;
   }
+  if (JOIN && c >= C) return;
   const int window = WIN ? hdr->window : 0;
   // tiles whose tokens all have kv_len 0 own no work unit: their rows are zero
   auto zero_rows = [&](int x0, int step) {

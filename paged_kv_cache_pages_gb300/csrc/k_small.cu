@@ -401,6 +401,9 @@ k_plan(const int32_t *__restrict__ tpt, int max_pages, const int32_t *__restrict
       for (int j = 0; j < 8; ++j) pg[j] = j < npg ? row[j] : -1;
       dec_start[4 * c + 2] = make_int4(pg[0], pg[1], pg[2], pg[3]);
       dec_start[4 * c + 3] = make_int4(pg[4], pg[5], pg[6], pg[7]);
+    } else {
+      // no record: nothing that the launch's early prefetch would follow
+      dec_start[4 * c] = make_int4(-1, -1, -1, -1);
     }
     if (W > 0 && c < Cp) {
       // unit w's place: tile, item, key block

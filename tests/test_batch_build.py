@@ -165,6 +165,7 @@ def test_refusals(pa):
         assert call(out=out) == pa.PA_EINVAL, i
     assert call(n=8193) == pa.PA_EUNSUPPORTED
     assert call(mp=1 << 20, P=1 << 12) == pa.PA_EUNSUPPORTED
+    assert call(N=2 ** 30) == pa.PA_EUNSUPPORTED
     assert call(pt=24) == pa.PA_EALIGN and call(ref=8) == pa.PA_EALIGN
     assert call(out=[P, P, P, P, 40, P, P]) == pa.PA_EALIGN
 

@@ -217,6 +217,9 @@ def test_bad_pages_and_foreign_plans_are_flagged(pa):
     pa.plan_diff(g.tpt, g.kv, 4, 2, 16, 64, ws)                  # and the other way round
     pa.prefill(g.q, g.kp, g.vp, g.tpt, g.kv, 0.2, out, ws)
     assert pa.read_error(ws) == pa.PA_ERR_PLAN and out.eq(3).all()
+    pa.plan_diff(g.tpt[:-1], g.kv[:-1], 4, 2, 16, 64, ws)        # one of other sizes
+    pa.diff_run(*args, out=out, workspace=ws)
+    assert pa.read_error(ws) == pa.PA_ERR_PLAN and out.eq(3).all()
     tpt = g.tpt.clone()
     tpt[:, 1] = case.num_pages + 5
     pa.diff_forward(*args[:3], tpt, *args[4:], out=out, workspace=ws)
@@ -243,6 +246,8 @@ def test_binding_refusals(pa):
         pa.diff_forward(*ok, norm_weight=torch.ones(case.d + 1, device="cuda"))
     with pytest.raises(ValueError):
         pa.diff_run(*ok)
+    with pytest.raises(ValueError):
+        pa.diff_forward(*ok[:6], None)
     inf, nan = float("inf"), float("nan")
     for scale in (0.0, -1.0, inf, nan):
         with pytest.raises(pa.PagedAttnError) as e:

@@ -214,6 +214,10 @@ def test_foreign_plans_and_bad_pages_are_flagged(pa):
     pa.plan_window(g.tpt, g.kv, 4, 2, 16, 64, 21, ws)
     pa.prefill(*args, out, ws)
     assert pa.read_error(ws) == pa.PA_ERR_PLAN and out.eq(3).all()
+    wider = torch.nn.functional.pad(g.tpt, (0, 3), value=-1)     # a plan of other sizes
+    pa.plan_window(wider, g.kv, 4, 2, 16, 64, 21, ws)
+    pa.window_run(*args, out=out, workspace=ws)
+    assert pa.read_error(ws) == pa.PA_ERR_PLAN and out.eq(3).all()
     tpt = g.tpt.clone()
     tpt[:40, 5] = case.num_pages                     # positions 80..95: inside the windows
     pa.window_forward(*args[:3], tpt, *args[4:], 21, out=out, workspace=ws)
