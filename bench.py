@@ -40,14 +40,19 @@ METRIC = "decode KV GB/s + prefill TFLOP/s, Qwen3-8B-shape paged attn, 8×16K, 1
 # k_decode_fp8_longtail: one FP8 launch of `profile_case fp8` / `fp8_longtail`; k_copy_pages: one launch of `profile_case copy` (writes still
 # in L2 at the end of the launch are not counted).  Summaries and commands: profiles/.
 TRAFFIC = {
-    "k_prefill": {"bytes": 397.60e6, "files": ["k_prefill.cu"], "digest": "d64645999e60d5cd"},
-    "k_prefill_fp8": {"bytes": 216.40e6, "files": ["k_prefill.cu"], "digest": "d64645999e60d5cd"},
-    "k_decode": {"bytes": 86.21e6, "files": ["k_decode.cu"], "digest": "7c09222e8332d9bc"},
-    "k_decode_longtail": {"bytes": 1081.85e6, "files": ["k_decode.cu"], "digest": "7c09222e8332d9bc"},
-    "k_decode_span": {"bytes": 116.18e6, "files": ["k_decode.cu"], "digest": "7c09222e8332d9bc"},
-    "k_decode_fp8": {"bytes": 43.68e6, "files": ["k_decode.cu"], "digest": "7c09222e8332d9bc"},
-    "k_decode_fp8_longtail": {"bytes": 559.86e6, "files": ["k_decode.cu"], "digest": "7c09222e8332d9bc"},
-    "k_copy_pages": {"bytes": 488.15e6, "files": ["k_small.cu"], "digest": "8ffc91b37d609dbd"},
+    "k_prefill": {"bytes": 391.40e6, "files": ["k_prefill.cu"], "digest": "a6e0b685c170439d"},
+    "k_prefill_fp8": {"bytes": 206.23e6, "files": ["k_prefill.cu"], "digest": "a6e0b685c170439d"},
+    "k_decode": {"bytes": 86.17e6, "files": ["k_decode.cu", "join.cuh"],
+                 "digest": "9f2ece10d5d4f0de"},
+    "k_decode_longtail": {"bytes": 1082.10e6, "files": ["k_decode.cu", "join.cuh"],
+                          "digest": "9f2ece10d5d4f0de"},
+    "k_decode_span": {"bytes": 116.18e6, "files": ["k_decode.cu", "join.cuh"],
+                      "digest": "9f2ece10d5d4f0de"},
+    "k_decode_fp8": {"bytes": 43.67e6, "files": ["k_decode.cu", "join.cuh"],
+                     "digest": "9f2ece10d5d4f0de"},
+    "k_decode_fp8_longtail": {"bytes": 560.29e6, "files": ["k_decode.cu", "join.cuh"],
+                              "digest": "9f2ece10d5d4f0de"},
+    "k_copy_pages": {"bytes": 488.05e6, "files": ["k_small.cu"], "digest": "16baa70ee4095a73"},
 }
 _TRAFFIC_HEADERS = ["common.cuh", "tc.cuh", "tmap.cuh", "kernels.cuh"]
 
