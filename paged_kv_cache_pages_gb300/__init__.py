@@ -145,6 +145,19 @@ def _raw_stream(stream, device):
         else stream.cuda_stream
 
 
+def _used_on(stream, *made):
+    """Buffers made here for a call on another stream than the current one stay allocated
+    until that stream is past the call."""
+    if stream is not None:
+        for t in made:
+            t.record_stream(stream)
+
+
+def _int32(n):
+    """`n` held to int32 (ctypes would wrap it): "all" from the largest on, refused below 1."""
+    return max(min(int(n), 2 ** 31 - 1), -1)
+
+
 def _req(t, dtype, name):
     if not (t.is_cuda and t.dtype == dtype and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
@@ -250,6 +263,7 @@ def batch_build(seq_page_table, seq_len, new_len, page_ref, P, T, out=None, err=
              (page_ref, i32, (num_pages,), "page_ref"))
     if out is None:
         out = new_batch(n_seq, max_pages, T, dev)
+        _used_on(stream, *out)
     else:
         _req_all(dev, (out[0], i32, (n_seq + 1,), "q_start"),
                  (out[1], i32, (n_seq,), "seq_len (out)"), (out[2], i32, (T,), "tok_seq"),
@@ -520,7 +534,7 @@ def plan_diff(tok_page_table, tok_kv_len, Hq, Hkv, P, d, workspace, stream=None)
 
 def plan_window(tok_page_table, tok_kv_len, Hq, Hkv, P, d, window, workspace, stream=None):
     """plan for window_run: every token attends to its last `window` positions."""
-    _plan("paged_attn_plan_window", tok_page_table, tok_kv_len, Hq, Hkv, P, d, (int(window),),
+    _plan("paged_attn_plan_window", tok_page_table, tok_kv_len, Hq, Hkv, P, d, (_int32(window),),
           workspace, stream)
 
 
@@ -542,10 +556,12 @@ def _attn_on(fn_name, q, k_pages, v_pages, tok_page_table, tok_kv_len, scale, ex
             _req_on(t, torch.float32, (n,), dev, name)
     if out is None:
         out = torch.empty_like(q)
+        _used_on(stream, out)
     else:
         _req_on(out, torch.float16, (T, Hq, d), dev, "out")
     if workspace is None:
         workspace = new_ws(T, Hq, Hkv, d, dev)
+        _used_on(stream, workspace)
     else:
         _req_on(workspace, torch.uint8, (workspace.numel(),), dev, "workspace")
     _call(fn_name, getattr(_lib, fn_name), dev,
@@ -599,7 +615,7 @@ def window_forward(q, k_pages, v_pages, tok_page_table, tok_kv_len, scale, windo
                    out=None, workspace=None, stream=None):
     """plan_window then window_run for one ubatch; returns out [T][Hq][d] float16."""
     return _attn_on("paged_attn_window_forward", q, k_pages, v_pages, tok_page_table, tok_kv_len,
-                    scale, (int(window), None if sink is None else sink.data_ptr()),
+                    scale, (_int32(window), None if sink is None else sink.data_ptr()),
                     ((sink, q.shape[1], "sink"),), out, workspace, new_workspace, stream)
 
 

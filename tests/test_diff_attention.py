@@ -268,6 +268,69 @@ def test_binding_refusals(pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["diff", "window"])
+def test_waits_that_give_up_end_the_launch(pa, kind):
+    """With a limit of 1 us the split-KV launch's waits give up: the call ends with
+    PA_ERR_TIMEOUT (small cases, beside a prefill of 120 tokens and without one, may end in
+    time: a CTA has a block or two), and the next call at the usual limit is right."""
+    def run(case, g, ws):
+        if kind == "diff":
+            lam, w, eps, c = params(33, case.Hq, 128)
+            return pa.diff_forward(g.q, g.kp, g.vp, g.tpt, g.kv, 0.125, cuda(lam), cuda(w), eps,
+                                   c, workspace=ws)
+        return pa.window_forward(g.q, g.kp, g.vp, g.tpt, g.kv, 0.125, 2222, workspace=ws)
+
+    def short_of_time(case, g, ws):
+        old = pa.set_decode_wait_limit(1000)
+        try:
+            run(case, g, ws)
+            return pa.read_error(ws)
+        finally:
+            pa.set_decode_wait_limit(old)
+
+    for chunks in (((0, 500, 120),), ()):
+        case = workloads.small_prefill(33, P=16, d=128, Hq=4, Hkv=2, chunks=chunks, extra_decode=6)
+        g, r = whole(pa, case)
+        lam, w, eps, c = params(33, 4, 128)
+        ws = pa.new_diff_workspace(case.T, 4, 2, 128)
+        assert short_of_time(case, g, ws) in (0, pa.PA_ERR_TIMEOUT)
+        y = run(case, g, ws)
+        assert pa.read_error(ws) == 0
+        want, tol = (ref64.diff_attention(case.q, r["kp"], r["vp"], r["tpt"], r["kv"], 0.125, lam, w,
+                                          eps, c) if kind == "diff" else
+                     ref64.window_attention(case.q, r["kp"], r["vp"], r["tpt"], r["kv"], 0.125,
+                                            2222))
+        ref64.assert_within(y.cpu().numpy(), want, tol, kind)
+    case = workloads.decode(0)
+    g = GpuCase(pa, case)
+    ws = pa.new_diff_workspace(case.T, case.Hq, case.Hkv, 128)
+    y = run(case, g, ws)
+    assert pa.read_error(ws) == 0
+    assert short_of_time(case, g, ws) == pa.PA_ERR_TIMEOUT
+    assert torch.equal(run(case, g, ws), y) and pa.read_error(ws) == 0
+
+
+@pytest.mark.gpu
+def test_buffers_made_by_a_call_on_another_stream(pa):
+    """No output and no workspace given, on another stream than the current one, while the
+    current one allocates: the call's buffers are not handed out again under it."""
+    case = workloads.small_prefill(34, P=16, d=64, Hq=4, Hkv=2, chunks=((0, 400, 90),))
+    g, r = whole(pa, case)
+    lam, w, eps, c = params(34, 4, 64)
+    dl, dw, s = cuda(lam), cuda(w), torch.cuda.Stream()
+    want, tol = ref64.diff_attention(case.q, r["kp"], r["vp"], r["tpt"], r["kv"], 0.2, lam, w, eps, c)
+    torch.cuda.synchronize()
+    ys = []
+    for _ in range(10):
+        ys.append(pa.diff_forward(g.q, g.kp, g.vp, g.tpt, g.kv, 0.2, dl, dw, eps, c, stream=s))
+        junk = torch.full((1 << 26,), 255, dtype=torch.uint8, device="cuda")
+        del junk
+    torch.cuda.synchronize()
+    for y in ys:
+        ref64.assert_within(y.cpu().numpy(), want, tol)
+
+
+@pytest.mark.gpu
 def test_two_graphs_share_a_workspace_on_another_stream(pa):
     """Two captured steps of different ubatches in one workspace, replayed in turn."""
     s = torch.cuda.Stream()

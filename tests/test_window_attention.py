@@ -107,6 +107,11 @@ def test_tiny(pa, min_run, route, window):
     case = workloads.tiny(1)
     g, r = whole(pa, case)
     check(pa, g, case, r, window, what="no sink")
+    if window == 1 << 30:  # a window that no int32 holds is "all" too
+        check(pa, g, case, r, (1 << 33) + 5, what="wide")
+        with pytest.raises(pa.PagedAttnError) as e:
+            check(pa, g, case, r, 5 - (1 << 33), what="negative")
+        assert e.value.status == pa.PA_EINVAL
     check(pa, g, case, r, window, sinks(case.Hq), what="sink")
 
 
