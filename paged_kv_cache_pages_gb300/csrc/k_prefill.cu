@@ -595,13 +595,22 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   constexpr bool DIFF = VAR == kPfDiff, WIN = VAR == kPfWin;
   // How a block's products overlap its softmax.  SPLIT (d 64, whose accumulators leave 128 TMEM
   // columns): P has columns of its own, so that S of the next block is computed while the softmax
-  // works on this one; four 512-token chunks 361 to 340 us (differential), 207 to 192 us
-  // (windowed), nothing lost at short ones.  HALF: the products of a block's first 64 keys start
-  // while the softmax computes the other half of P; windowed chunks at d 128 138 to 127 us, but
-  // differential ones, whose blocks have fewer MMAs to hide behind the second hand-off, 413 to
-  // 421 us, so they keep one.
-  constexpr bool SPLIT = (DIFF || WIN) && D == 64;
+  // works on this one; windowed, four 512-token chunks 207 to 192 us, nothing lost at short ones
+  // (differential tiles need S's columns for P's low part).  HALF: the products of a block's
+  // first 64 keys start while the softmax computes the other half of P; windowed chunks at d 128
+  // 138 to 127 us, but differential ones, whose blocks have fewer MMAs to hide behind the second
+  // hand-off, 413 to 421 us, so they keep one.
+  constexpr bool SPLIT = WIN && D == 64;
   constexpr bool HALF = WIN && !SPLIT;
+  // DIFF: of a block's first kLow keys the products also take what P's rounding to binary16 left
+  // (p - hi, itself rounded: 2^-22 of p).  The difference cancels part of two results but none of
+  // the rounding errors of their P, which weighed 1.2 times those of one softmax: 3.2e-4 of the
+  // result in all, 1.54 times the output's own rounding.  A quarter of the keys brings that to
+  // 2.96e-4, what the other attentions' tiles have.  It costs 9% of four 512-token chunks at up
+  // to 16K (412 to 450 us; d 64: 357 to 414) and 3% of three of 229 tokens; half the keys give
+  // 2.7e-4 for 23%, all of them in the first map 2.4e-4 for 35%: each 16 keys are 64 cycles of a
+  // block's MMA chain.
+  constexpr int kLow = DIFF ? 32 : 0;
   constexpr bool JOIN = DIFF || WIN;  // split items are joined by the split-KV launch (join.cuh)
   constexpr int kItemHeads = DIFF ? 1 : 2;
   static_assert(!KV8 || D == 128, "FP8 pages: d 128");
@@ -856,7 +865,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
       const uint32_t d = tmem + 256 + i * D;
       const uint32_t p = SPLIT ? tmem + 384 + i * 64 : tmem + i * 128;
       const uint32_t b0 = tc::opaque(st ? lV1 : lV0);
-      if constexpr (HALF || (SPLIT && WIN)) {
+      if constexpr (HALF || SPLIT) {
         if (SPLIT && nk - k0 == 8) {
           tc::mma_ts_lo_pred(d, p, b0, idPV, acc ? 1u : 0u);
 #pragma unroll
@@ -873,6 +882,9 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
         return;
       }
       tc::mma_ts_lo_pred(d, p, b0, idPV, acc ? 1u : 0u);
+#pragma unroll
+      for (int kk = 0; kk < kLow / 16; ++kk)  // P's low part, behind its 64 columns
+        if (kk < nk) tc::mma_ts_lo<1>(d, p + 64 + kk * 8, b0 + kk * 128, idPV);
 #pragma unroll
       for (int kk = 1; kk < KB / 16; ++kk) {
         // a 16-key step: 16 rows of the MN-major tile, or 32 bytes along the K-major rows
@@ -1177,7 +1189,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
           }
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {
-            uint32_t pk[16];
+            uint32_t pk[16], lo[16];
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
               const int c = 32 * q4 + j;
@@ -1186,10 +1198,20 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
               float2 p = make_float2(exp2_approx(x.x), exp2_approx(x.y));
               rs2 = fadd2(rs2, p);
               if (KV8) p = fmul2(p, vs2[c >> 1]);
+              if (c < kLow) {
+                // cut at binary16's 10 bits (its conversion is exact then), and the rest
+                const float2 hi = make_float2(__uint_as_float(__float_as_uint(p.x) & 0xffffe000u),
+                                              __uint_as_float(__float_as_uint(p.y) & 0xffffe000u));
+                const float2 r = ffma2(hi, make_float2(-1.f, -1.f), p);
+                const __half2 hr = __floats2half2_rn(r.x, r.y);
+                lo[j >> 1] = *reinterpret_cast<const uint32_t *>(&hr);
+                p = hi;
+              }
               __half2 hp = __floats2half2_rn(p.x, p.y);
               pk[j >> 1] = *reinterpret_cast<uint32_t *>(&hp);
             }
             tc::st16(tP + 16 * q4, pk);
+            if (32 * q4 < kLow) tc::st16(tP + 64 + 16 * q4, lo);
             if (HALF && q4 == 1) {
               // half of P: its products may start while the other half is computed
               rescale_o();

@@ -268,6 +268,38 @@ def test_binding_refusals(pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_error_of_the_tiles(pa, d):
+    """The error's norm is what two roundings leave.  A rounding to binary16 is off by a uniform
+    share of half a step, so by 2^-11 / sqrt(3) of 1 / the mantissa; over mantissas spread evenly
+    in their logarithm the mean square of that is 2^-22 / 3 * 0.75 / (2 ln 2).  P's rounding adds
+    it times (p v)^2 for each key of each map, but for the first 32 of a block of 128, whose
+    low part the products take; the output's adds it times y^2.  5% for the sample."""
+    case = workloads.small_prefill(35, P=16, d=d, Hq=4, Hkv=2, chunks=((0, 400, 181),),
+                                   extra_decode=0)
+    g, r = whole(pa, case)
+    lam, e, scale = params(35, 4, d)[0], d // 2, 1 / np.sqrt(d // 2)
+    got = pa.diff_forward(g.q, g.kp, g.vp, g.tpt, g.kv, scale, cuda(lam)).cpu().numpy()
+    q, step2 = ref64.f64(case.q), 2.0 ** -22 / 3 * 0.75 / (2 * np.log(2))
+    off = of_p = of_y = 0.0
+    for t in range(case.T):
+        for kv_head in range(2):
+            K, V = (ref64.rows_of(p, r["tpt"][t], 0, r["kv"][t], 16, kv_head)
+                    for p in (r["kp"], r["vp"]))
+            h = slice(2 * kv_head, 2 * kv_head + 2)
+            a1, a2 = (ref64.weighted(q[t, h, i:i + e], K[:, i:i + e], np.eye(len(K)), scale)[0]
+                      for i in (0, e))
+            a2 = a2 * lam[h, None]
+            y = (a1 - a2) @ V
+            rounded = np.arange(len(K)) % 128 >= 32
+            of_p += step2 * (((a1 ** 2 + a2 ** 2) * rounded) @ (V ** 2)).sum()
+            of_y += step2 * (y ** 2).sum()
+            off += ((got[t, h].astype(np.float64) - y) ** 2).sum()
+    assert off <= 1.05 ** 2 * (of_p + of_y), (off, of_p, of_y)
+    assert of_p < 1.2 * of_y  # P's rounding weighs about what the output's does
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["diff", "window"])
 def test_waits_that_give_up_end_the_launch(pa, kind):
     """With a limit of 1 us the split-KV launch's waits give up: the call ends with
