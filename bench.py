@@ -40,8 +40,8 @@ METRIC = "decode KV GB/s + prefill TFLOP/s, Qwen3-8B-shape paged attn, 8×16K, 1
 # k_decode_fp8_longtail: one FP8 launch of `profile_case fp8` / `fp8_longtail`; k_copy_pages: one launch of `profile_case copy` (writes still
 # in L2 at the end of the launch are not counted).  Summaries and commands: profiles/.
 TRAFFIC = {
-    "k_prefill": {"bytes": 391.40e6, "files": ["k_prefill.cu"], "digest": "a6e0b685c170439d"},
-    "k_prefill_fp8": {"bytes": 206.23e6, "files": ["k_prefill.cu"], "digest": "a6e0b685c170439d"},
+    "k_prefill": {"bytes": 398.35e6, "files": ["k_prefill.cu"], "digest": "64a55e556644666c"},
+    "k_prefill_fp8": {"bytes": 217.48e6, "files": ["k_prefill.cu"], "digest": "64a55e556644666c"},
     "k_decode": {"bytes": 86.17e6, "files": ["k_decode.cu", "join.cuh"],
                  "digest": "9f2ece10d5d4f0de"},
     "k_decode_longtail": {"bytes": 1082.10e6, "files": ["k_decode.cu", "join.cuh"],

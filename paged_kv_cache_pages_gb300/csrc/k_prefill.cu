@@ -599,7 +599,7 @@ k_prefill(AttnArgs a, const __grid_constant__ AttnMaps maps) {
   // (differential tiles need S's columns for P's low part).  HALF: the products of a block's
   // first 64 keys start while the softmax computes the other half of P; windowed chunks at d 128
   // 138 to 127 us, but differential ones, whose blocks have fewer MMAs to hide behind the second
-  // hand-off, 413 to 421 us, so they keep one.
+  // hand-off, 451 to 455 us (P's low part among the first products), so they keep one.
   constexpr bool SPLIT = WIN && D == 64;
   constexpr bool HALF = WIN && !SPLIT;
   // DIFF: of a block's first kLow keys the products also take what P's rounding to binary16 left
